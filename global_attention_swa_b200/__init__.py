@@ -9,6 +9,10 @@ Entry points (same names as the C ABI):
 
 * ``mimo_attn_prefill(q, k, v, sinks, window, cu_seqlens, max_seqlen, ...)``
 * ``mimo_attn_decode(q, k_cache, v_cache, seqlens, window, sinks, ...)``
+* ``mimo_attn_paged_attention(q, k_pages, v_pages, block_table, cu_seqlens_q, seqlens, ...)``
+  with ``mimo_attn_paged_append``, ``mimo_attn_page_hold``, ``mimo_attn_page_fork``,
+  ``mimo_attn_page_compact`` and ``mimo_attn_page_copy``: the paged cache
+  (``paged_cache.PagedCache`` keeps one)
 * ``mimo_attn_decode_workspace_size(...)``, ``mimo_attn_device_status(...)``
 """
 
@@ -52,6 +56,15 @@ EXPORTED = (
     "mimo_attn_decode_merge",
     "mimo_attn_prefill_backward_workspace_size",
     "mimo_attn_prefill_backward",
+    "mimo_attn_paged_attention_workspace_size",
+    "mimo_attn_paged_attention",
+    "mimo_attn_paged_append",
+    "mimo_attn_page_hold_workspace_size",
+    "mimo_attn_page_hold",
+    "mimo_attn_page_fork",
+    "mimo_attn_page_compact_workspace_size",
+    "mimo_attn_page_compact",
+    "mimo_attn_page_copy",
     "mimo_attn_wait_selftest",
     "mimo_attn_is_checked_build",
     "mimo_attn_checked_site",
@@ -112,6 +125,26 @@ def _load():
     lib.mimo_attn_prefill_backward.argtypes = [dp, vp, vp, vp, vp, vp, vp, vp, i32, vp, i32, i32, i32,
                                                vp, vp, vp, vp, vp, sz, vp]
     lib.mimo_attn_prefill_backward.restype = i32
+    lib.mimo_attn_paged_attention_workspace_size.argtypes = [dp, i32, i32, i32]
+    lib.mimo_attn_paged_attention_workspace_size.restype = sz
+    lib.mimo_attn_paged_attention.argtypes = [dp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32,
+                                              i32, vp, vp, vp, vp, sz, vp]
+    lib.mimo_attn_paged_attention.restype = i32
+    lib.mimo_attn_paged_append.argtypes = [dp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32,
+                                           ctypes.c_float, i32, vp]
+    lib.mimo_attn_paged_append.restype = i32
+    lib.mimo_attn_page_hold_workspace_size.argtypes = [i32]
+    lib.mimo_attn_page_hold_workspace_size.restype = sz
+    lib.mimo_attn_page_hold.argtypes = [vp, i32, vp, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.mimo_attn_page_hold.restype = i32
+    lib.mimo_attn_page_fork.argtypes = [vp, i32, vp, i32, i32, vp, i32, vp, vp, vp]
+    lib.mimo_attn_page_fork.restype = i32
+    lib.mimo_attn_page_compact_workspace_size.argtypes = [i32]
+    lib.mimo_attn_page_compact_workspace_size.restype = sz
+    lib.mimo_attn_page_compact.argtypes = [vp, i32, vp, i32, i32, i32, vp, vp, vp, vp, vp, sz, vp]
+    lib.mimo_attn_page_compact.restype = i32
+    lib.mimo_attn_page_copy.argtypes = [dp, vp, vp, i32, i32, i32, vp, i32, vp]
+    lib.mimo_attn_page_copy.restype = i32
     lib.mimo_attn_wait_selftest.argtypes = [vp]
     lib.mimo_attn_wait_selftest.restype = i32
     lib.mimo_attn_is_checked_build.argtypes = []
@@ -403,6 +436,225 @@ def mimo_attn_prefill_backward(q, k, v, out, lse, dout, sinks, window, cu_seqlen
                                               _ptr(dk), _ptr(dv), _ptr(ds), _ptr(ws), ws.numel(),
                                               _stream(stream, dev)))
     return dq, dk, dv, ds
+
+
+def _paged_shapes(k_pages, v_pages, hkv, dqk, dv, block_table, cu_seqlens_q, seqlens):
+    """The pools and tables of a paged cache agree with each other."""
+    if k_pages.dim() != 4 or v_pages.dim() != 4:
+        raise ValueError("k_pages and v_pages must be [num_pages, page_size, Hkv, D]")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [num_seqs, max_pages]")
+    _shape(k_pages, (k_pages.shape[0], k_pages.shape[1], hkv, dqk), "k_pages")
+    _shape(v_pages, (k_pages.shape[0], k_pages.shape[1], hkv, dv), "v_pages")
+    _shape(cu_seqlens_q, (block_table.shape[0] + 1,), "cu_seqlens_q")
+    _shape(seqlens, (block_table.shape[0],), "seqlens")
+
+
+def mimo_attn_paged_attention_workspace_size(hq, hkv, num_seqs, total_q, max_seqlen_q, dqk=192, dv=128):
+    dims = make_dims(hq, hkv, dqk, dv)
+    return int(lib.mimo_attn_paged_attention_workspace_size(ctypes.byref(dims), num_seqs, total_q,
+                                                            max_seqlen_q))
+
+
+def mimo_attn_paged_attention(q, k_pages, v_pages, block_table, cu_seqlens_q, seqlens, max_seqlen_q,
+                              window, sinks, out=None, lse=None, workspace=None,
+                              out_dtype=torch.bfloat16, softmax_scale=None, v_scale=1.0,
+                              return_lse=True, stream=None):
+    """Attention of each sequence's new tokens over its paged cache (chunked prefill,
+    drafted tokens, decode; see include/mimo_attn.h).  q [Nt,Hq,192] bf16 packed by
+    cu_seqlens_q [B+1]; k_pages / v_pages [P,page_size,Hkv,192/128] bf16; block_table
+    [B,max_pages] and seqlens [B] (the new tokens included) int32.
+
+    Returns (out [Nt,Hq,128], lse [Hq,Nt] fp32 or None).
+    """
+    nt, hq, dqk = q.shape
+    hkv, dv = k_pages.shape[-2], v_pages.shape[-1]
+    _paged_shapes(k_pages, v_pages, hkv, dqk, dv, block_table, cu_seqlens_q, seqlens)
+    _shape(sinks, (hq,), "sinks")
+    _shape(out, (nt, hq, dv), "out")
+    _shape(lse, (hq, nt), "lse")
+    dev = q.device
+    if out is None:
+        out = torch.empty((nt, hq, dv), dtype=out_dtype, device=dev)
+    if lse is None and return_lse:
+        lse = torch.empty((hq, nt), dtype=torch.float32, device=dev)
+    dims = make_dims(hq, hkv, dqk, dv, softmax_scale, v_scale, out.dtype)
+    B, M = block_table.shape
+    need = int(lib.mimo_attn_paged_attention_workspace_size(ctypes.byref(dims), B, nt, int(max_seqlen_q)))
+    if need and workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _same_device(dev, k_pages=k_pages, v_pages=v_pages, block_table=block_table,
+                 cu_seqlens_q=cu_seqlens_q, seqlens=seqlens, sinks=sinks, out=out, lse=lse,
+                 workspace=workspace)
+    wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    with _on_device(dev):
+        _check(lib.mimo_attn_paged_attention(
+            ctypes.byref(dims), _ptr(q, "q", _BF16), _ptr(k_pages, "k_pages", _BF16),
+            _ptr(v_pages, "v_pages", _BF16), _ptr(block_table, "block_table", _I32),
+            _ptr(cu_seqlens_q, "cu_seqlens_q", _I32), _ptr(seqlens, "seqlens", _I32), B, nt,
+            int(max_seqlen_q), k_pages.shape[0], k_pages.shape[1], M, int(window),
+            _ptr(sinks, "sinks", _F32), _ptr(out, "out", _OUT), _ptr(lse, "lse", _F32),
+            _ptr(workspace, "workspace"), wbytes, _stream(stream, dev)))
+    return out, lse
+
+
+def mimo_attn_paged_append(q, k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q, seqlens,
+                           rope_theta, rotary_dim=None, q_out=None, stream=None):
+    """Rotate the new tokens' q and k and write k, v into their pages (see
+    include/mimo_attn.h).  Returns the rotated q: ``q_out`` (which may be q), or a new tensor."""
+    nt, hq, dqk = q.shape
+    hkv, dv = k_pages.shape[-2], v_pages.shape[-1]
+    _paged_shapes(k_pages, v_pages, hkv, dqk, dv, block_table, cu_seqlens_q, seqlens)
+    _shape(k_new, (nt, hkv, dqk), "k_new")
+    _shape(v_new, (nt, hkv, dv), "v_new")
+    _shape(q_out, (nt, hq, dqk), "q_out")
+    dev = q.device
+    if q_out is None:
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    _same_device(dev, q_out=q_out, k_new=k_new, v_new=v_new, k_pages=k_pages, v_pages=v_pages,
+                 block_table=block_table, cu_seqlens_q=cu_seqlens_q, seqlens=seqlens)
+    dims = make_dims(hq, hkv, dqk, dv)
+    rd = dqk if rotary_dim is None else int(rotary_dim)
+    B, M = block_table.shape
+    with _on_device(dev):
+        _check(lib.mimo_attn_paged_append(
+            ctypes.byref(dims), _ptr(q, "q", _BF16), _ptr(q_out, "q_out", _BF16),
+            _ptr(k_new, "k_new", _BF16), _ptr(v_new, "v_new", _BF16),
+            _ptr(k_pages, "k_pages", _BF16), _ptr(v_pages, "v_pages", _BF16),
+            _ptr(block_table, "block_table", _I32), _ptr(cu_seqlens_q, "cu_seqlens_q", _I32),
+            _ptr(seqlens, "seqlens", _I32), B, nt, k_pages.shape[0], k_pages.shape[1], M,
+            float(rope_theta), rd, _stream(stream, dev)))
+    return q_out
+
+
+def _page_table_shapes(page_refs, block_table, refs_out, table_out, rows_out):
+    if page_refs.dim() != 1 or block_table.dim() != 2:
+        raise ValueError("page_refs must be [num_pages] and block_table [num_seqs, max_pages]")
+    _shape(refs_out, page_refs.shape, "refs_out")
+    _shape(table_out, (rows_out, block_table.shape[1]), "table_out")
+
+
+def mimo_attn_page_hold(page_refs, block_table, seqlens, page_size, first=None, write_from=None,
+                        refs_out=None, table_out=None, moves=None, info=None, workspace=None,
+                        stream=None):
+    """Make each sequence hold exactly the pages of positions [first, seqlens), those from
+    write_from on its own (see include/mimo_attn.h).  refs_out / table_out may be
+    page_refs / block_table (in place); None allocates them.
+
+    Returns (refs_out, table_out, moves [B,2] for mimo_attn_page_copy, info [2]: pages
+    missing (nothing was changed if > 0), pages free afterwards).
+    """
+    B, M = block_table.shape
+    _page_table_shapes(page_refs, block_table, refs_out, table_out, B)
+    for name, t in (("seqlens", seqlens), ("first", first), ("write_from", write_from)):
+        _shape(t, (B,), name)
+    _shape(moves, (B, 2), "moves")
+    _shape(info, (2,), "info")
+    dev = page_refs.device
+    if refs_out is None:
+        refs_out = torch.empty_like(page_refs)
+    if table_out is None:
+        table_out = torch.empty_like(block_table, memory_format=torch.contiguous_format)
+    if moves is None:
+        moves = torch.empty((B, 2), dtype=torch.int32, device=dev)
+    if info is None:
+        info = torch.empty(2, dtype=torch.int32, device=dev)
+    need = int(lib.mimo_attn_page_hold_workspace_size(page_refs.numel()))
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _same_device(dev, block_table=block_table, seqlens=seqlens, first=first, write_from=write_from,
+                 refs_out=refs_out, table_out=table_out, moves=moves, info=info, workspace=workspace)
+    with _on_device(dev):
+        _check(lib.mimo_attn_page_hold(
+            _ptr(page_refs, "page_refs", _I32), page_refs.numel(),
+            _ptr(block_table, "block_table", _I32), B, M, int(page_size),
+            _ptr(seqlens, "seqlens", _I32), _ptr(first, "first", _I32),
+            _ptr(write_from, "write_from", _I32), _ptr(refs_out, "refs_out", _I32),
+            _ptr(table_out, "table_out", _I32), _ptr(moves, "moves", _I32), _ptr(info, "info", _I32),
+            _ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+            _stream(stream, dev)))
+    return refs_out, table_out, moves, info
+
+
+def mimo_attn_page_fork(page_refs, block_table, parent, refs_out=None, table_out=None, stream=None):
+    """Row i of the new table is row parent[i] of block_table, empty where parent[i] < 0
+    (see include/mimo_attn.h).  refs_out may be page_refs (in place); table_out may not
+    be block_table.  Returns (refs_out, table_out)."""
+    if parent.dim() != 1:
+        raise ValueError("parent must be 1-D")
+    B, M = block_table.shape
+    n = parent.numel()
+    _page_table_shapes(page_refs, block_table, refs_out, table_out, n)
+    dev = page_refs.device
+    if refs_out is None:
+        refs_out = torch.empty_like(page_refs)
+    if table_out is None:
+        table_out = torch.empty((n, M), dtype=torch.int32, device=dev)
+    _same_device(dev, block_table=block_table, parent=parent, refs_out=refs_out, table_out=table_out)
+    with _on_device(dev):
+        _check(lib.mimo_attn_page_fork(
+            _ptr(page_refs, "page_refs", _I32), page_refs.numel(),
+            _ptr(block_table, "block_table", _I32), B, M, _ptr(parent, "parent", _I32), n,
+            _ptr(refs_out, "refs_out", _I32), _ptr(table_out, "table_out", _I32),
+            _stream(stream, dev)))
+    return refs_out, table_out
+
+
+def mimo_attn_page_compact(page_refs, block_table, max_moves, refs_out=None, table_out=None,
+                           moves=None, info=None, workspace=None, stream=None):
+    """Give the used pages at the end of the pool the free places at its front, at most
+    max_moves of them (see include/mimo_attn.h).  refs_out / table_out may be the inputs.
+
+    Returns (refs_out, table_out, moves [max_moves,2] for mimo_attn_page_copy, info [2]:
+    moves made, pages in use).
+    """
+    B, M = block_table.shape
+    _page_table_shapes(page_refs, block_table, refs_out, table_out, B)
+    max_moves = int(max_moves)
+    _shape(moves, (max_moves, 2), "moves")
+    _shape(info, (2,), "info")
+    dev = page_refs.device
+    if refs_out is None:
+        refs_out = torch.empty_like(page_refs)
+    if table_out is None:
+        table_out = torch.empty_like(block_table, memory_format=torch.contiguous_format)
+    if moves is None:
+        moves = torch.empty((max_moves, 2), dtype=torch.int32, device=dev)
+    if info is None:
+        info = torch.empty(2, dtype=torch.int32, device=dev)
+    need = int(lib.mimo_attn_page_compact_workspace_size(page_refs.numel()))
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _same_device(dev, block_table=block_table, refs_out=refs_out, table_out=table_out, moves=moves,
+                 info=info, workspace=workspace)
+    with _on_device(dev):
+        _check(lib.mimo_attn_page_compact(
+            _ptr(page_refs, "page_refs", _I32), page_refs.numel(),
+            _ptr(block_table, "block_table", _I32), B, M, max_moves,
+            _ptr(refs_out, "refs_out", _I32), _ptr(table_out, "table_out", _I32),
+            _ptr(moves, "moves", _I32), _ptr(info, "info", _I32), _ptr(workspace, "workspace"),
+            workspace.numel() * workspace.element_size(), _stream(stream, dev)))
+    return refs_out, table_out, moves, info
+
+
+def mimo_attn_page_copy(k_pages, v_pages, moves, stream=None):
+    """Copy pages moves[:, 0] over pages moves[:, 1] in place (rows of -1 are skipped; see
+    include/mimo_attn.h).  k_pages / v_pages [P,page_size,Hkv,192/128] bf16 of one layer, or
+    [layers,P,...] of several.  Returns (k_pages, v_pages)."""
+    if k_pages.dim() not in (4, 5) or k_pages.dim() != v_pages.dim():
+        raise ValueError("k_pages and v_pages must be [num_pages, page_size, Hkv, D], or with a layer axis first")
+    _shape(v_pages, (*k_pages.shape[:-1], v_pages.shape[-1]), "v_pages")
+    _shape(moves, (moves.shape[0], 2), "moves")
+    P, ps, hkv, dqk = k_pages.shape[-4:]
+    dev = k_pages.device
+    _same_device(dev, v_pages=v_pages, moves=moves)
+    dims = make_dims(hkv, hkv, dqk, v_pages.shape[-1])
+    with _on_device(dev):
+        _check(lib.mimo_attn_page_copy(
+            ctypes.byref(dims), _ptr(k_pages, "k_pages", _BF16), _ptr(v_pages, "v_pages", _BF16),
+            k_pages.shape[0] if k_pages.dim() == 5 else 1, P, ps, _ptr(moves, "moves", _I32),
+            moves.shape[0], _stream(stream, dev)))
+    return k_pages, v_pages
 
 
 def _current_device():

@@ -21,6 +21,10 @@
 #include "decode_fp8_kernel.cuh"
 #include "rope_append_kernel.cuh"
 #include "decode_merge_kernel.cuh"
+#include "paged_attention_kernel.cuh"
+#include "paged_append_kernel.cuh"
+#include "page_table_kernel.cuh"
+#include "page_copy_kernel.cuh"
 #include "backward_kernel.cuh"
 #include "backward_tc_kernel.cuh"
 #include "backward_dq_tc_kernel.cuh"
@@ -871,6 +875,337 @@ mimo_status_t mimo_attn_set_device_status(int code, void* stream) {
                                                cudaMemcpyHostToDevice, (cudaStream_t)stream),
                        "write status")))
     return st;
+  return ok();
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- paged cache
+
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// The sizes and tables every call over a paged cache takes.
+mimo_status_t check_paged(const int32_t* block_table, const int32_t* cu_seqlens_q, const int32_t* seqlens,
+                          int num_seqs, int total_q, int max_seqlen_q, int num_pages, int page_size,
+                          int max_pages) {
+  if (num_seqs < 0 || total_q < 0 || max_seqlen_q < 0)
+    return fail(MIMO_ERR_INVALID_ARG, "sizes must be non-negative");
+  if (num_pages <= 0 || page_size <= 0 || max_pages <= 0)
+    return fail(MIMO_ERR_INVALID_ARG, "num_pages, page_size and max_pages must be positive");
+  if (page_size % 16) return fail(MIMO_ERR_UNSUPPORTED, "page_size must be a multiple of 16 (got %d)", page_size);
+  if ((long)num_pages * page_size > 0x7fffffffL || (long)max_pages * page_size > 0x7fffffffL)
+    return fail(MIMO_ERR_UNSUPPORTED, "num_pages * page_size and max_pages * page_size must fit in int32");
+  if (max_seqlen_q > total_q)
+    return fail(MIMO_ERR_INVALID_ARG, "max_seqlen_q (%d) > total_q (%d)", max_seqlen_q, total_q);
+  if (!block_table || !cu_seqlens_q || !seqlens)
+    return fail(MIMO_ERR_INVALID_ARG, "block_table, cu_seqlens_q and seqlens must be non-NULL");
+  if (!aligned4(block_table) || !aligned4(cu_seqlens_q) || !aligned4(seqlens))
+    return fail(MIMO_ERR_INVALID_ARG, "block_table, cu_seqlens_q and seqlens must be 4-byte aligned");
+  return MIMO_OK;
+}
+
+mimo::PagedBatch paged_batch(const int32_t* block_table, const int32_t* cu_seqlens_q, const int32_t* seqlens,
+                             int num_seqs, int total_q, int max_seqlen_q, int num_pages, int page_size,
+                             int max_pages) {
+  mimo::PagedBatch b;
+  b.table = block_table;
+  b.cu_q = cu_seqlens_q;
+  b.seqlens = seqlens;
+  b.num_seqs = num_seqs;
+  b.total_q = total_q;
+  b.max_q = max_seqlen_q;
+  b.num_pages = num_pages;
+  b.page_size = page_size;
+  b.max_pages = max_pages;
+  return b;
+}
+
+// The arrays of the page bookkeeping calls.
+mimo_status_t check_page_table(const int32_t* page_refs, int num_pages, const int32_t* block_table,
+                               int num_seqs, int max_pages, const int32_t* refs_out, const int32_t* table_out) {
+  if (num_pages <= 0) return fail(MIMO_ERR_INVALID_ARG, "num_pages must be positive (got %d)", num_pages);
+  if (num_seqs < 0 || max_pages < 0) return fail(MIMO_ERR_INVALID_ARG, "sizes must be non-negative");
+  if ((long)num_seqs * max_pages > 0x7fffffffL)
+    return fail(MIMO_ERR_UNSUPPORTED, "num_seqs * max_pages must fit in int32");
+  const bool entries = num_seqs > 0 && max_pages > 0;
+  if (!page_refs || !refs_out || (entries && (!block_table || !table_out)))
+    return fail(MIMO_ERR_INVALID_ARG, "page_refs, block_table and their outputs must be non-NULL");
+  if (!aligned4(page_refs) || !aligned4(refs_out) || !aligned4(block_table) || !aligned4(table_out))
+    return fail(MIMO_ERR_INVALID_ARG, "page_refs, block_table and their outputs must be 4-byte aligned");
+  return MIMO_OK;
+}
+
+// One cluster of CTAs over `elements` array elements: enough that each thread
+// passes over a few, at most the portable cluster size.
+template <typename Params>
+mimo_status_t launch_cluster(void (*kernel)(Params), const Params& p, long elements, void* stream, const char* what) {
+  int ctas = 1;
+  while (ctas < mimo::kPtMaxCtas && elements > (long)ctas * 2 * mimo::kPtThreads) ctas *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(mimo::kPtThreads);
+  cfg.stream = (cudaStream_t)stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = ctas;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cuda_check(cudaLaunchKernelEx(&cfg, kernel, p), what);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t mimo_attn_paged_attention_workspace_size(const mimo_attn_dims_t* dims, int num_seqs, int total_q,
+                                                int max_seqlen_q) {
+  (void)dims;
+  (void)num_seqs;
+  (void)total_q;
+  (void)max_seqlen_q;
+  return 0;
+}
+
+mimo_status_t mimo_attn_paged_attention(const mimo_attn_dims_t* dims, const void* q, const void* k_pages,
+                                        const void* v_pages, const int32_t* block_table,
+                                        const int32_t* cu_seqlens_q, const int32_t* seqlens, int num_seqs,
+                                        int total_q, int max_seqlen_q, int num_pages, int page_size,
+                                        int max_pages, int window, const float* sinks, void* out, float* lse,
+                                        void* workspace, size_t workspace_bytes, void* stream) {
+  NvtxRange nvtx_range("mimo_attn_paged_attention");
+  mimo_status_t st = check_dims(dims);
+  if (st) return st;
+  if (window < 0) return fail(MIMO_ERR_INVALID_ARG, "window must be >= 0 (got %d)", window);
+  if ((st = check_paged(block_table, cu_seqlens_q, seqlens, num_seqs, total_q, max_seqlen_q, num_pages,
+                        page_size, max_pages)))
+    return st;
+  const int Hq = dims->num_heads_q, Hkv = dims->num_heads_kv, G = Hq / Hkv;
+  if (G > 128) return fail(MIMO_ERR_UNSUPPORTED, "at most 128 query heads per key/value head (got %d)", G);
+  if (num_seqs == 0 || total_q == 0 || max_seqlen_q == 0) return ok();  // nothing to do
+  if (!q || !k_pages || !v_pages || !out)
+    return fail(MIMO_ERR_INVALID_ARG, "q, k_pages, v_pages and out must be non-NULL");
+  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) || !aligned4(lse) ||
+      !aligned4(sinks))
+    return fail(MIMO_ERR_INVALID_ARG, "q, k_pages, v_pages and out must be 16-byte aligned");
+  const size_t need = mimo_attn_paged_attention_workspace_size(dims, num_seqs, total_q, max_seqlen_q);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
+    return fail(MIMO_ERR_WORKSPACE, "workspace of %zu bytes, 16-byte aligned, is needed (got %zu)", need,
+                workspace ? workspace_bytes : (size_t)0);
+  mimo::PagedAttnParams p;
+  p.pb = paged_batch(block_table, cu_seqlens_q, seqlens, num_seqs, total_q, max_seqlen_q, num_pages, page_size,
+                     max_pages);
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k_pages);
+  p.v = static_cast<const __nv_bfloat16*>(v_pages);
+  p.sinks = sinks;
+  p.out = out;
+  p.lse = lse;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.G = G;
+  p.window = window;
+  p.scale_log2 = scale_log2_of(dims);
+  p.v_scale = v_scale_of(dims);
+  p.out_f32 = dims->out_dtype == MIMO_DTYPE_F32;
+  const long blocks = ((long)total_q * Hq + 7) / 8;
+  mimo::paged_attention_kernel<<<(int)std::min<long>(blocks, 8L * sm_count()), 256, 0, (cudaStream_t)stream>>>(p);
+  if ((st = cuda_check(cudaGetLastError(), "paged attention launch"))) return st;
+  return ok();
+}
+
+mimo_status_t mimo_attn_paged_append(const mimo_attn_dims_t* dims, const void* q, void* q_out,
+                                     const void* k_new, const void* v_new, void* k_pages, void* v_pages,
+                                     const int32_t* block_table, const int32_t* cu_seqlens_q,
+                                     const int32_t* seqlens, int num_seqs, int total_q, int num_pages,
+                                     int page_size, int max_pages, float rope_theta, int rotary_dim,
+                                     void* stream) {
+  NvtxRange nvtx_range("mimo_attn_paged_append");
+  mimo_status_t st = check_dims(dims);
+  if (st) return st;
+  if ((st = check_paged(block_table, cu_seqlens_q, seqlens, num_seqs, total_q, total_q, num_pages, page_size,
+                        max_pages)))
+    return st;
+  if (!(rope_theta > 0.f) || !std::isfinite(rope_theta))
+    return fail(MIMO_ERR_INVALID_ARG, "rope_theta must be positive and finite");
+  if (rotary_dim < 0 || rotary_dim > dims->head_dim_qk || (rotary_dim & 1))
+    return fail(MIMO_ERR_INVALID_ARG, "rotary_dim must be even and in [0, %d] (got %d)", dims->head_dim_qk,
+                rotary_dim);
+  if (num_seqs == 0 || total_q == 0) return ok();
+  if (!q || !q_out || !k_new || !v_new || !k_pages || !v_pages)
+    return fail(MIMO_ERR_INVALID_ARG, "q, q_out, k_new, v_new and the pages must be non-NULL");
+  if (!aligned16(q) || !aligned16(q_out) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(k_pages) ||
+      !aligned16(v_pages))
+    return fail(MIMO_ERR_INVALID_ARG, "q, q_out, k_new, v_new and the pages must be 16-byte aligned");
+  mimo::PagedAppendParams p;
+  p.pb = paged_batch(block_table, cu_seqlens_q, seqlens, num_seqs, total_q, total_q, num_pages, page_size,
+                     max_pages);
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.q_out = static_cast<__nv_bfloat16*>(q_out);
+  p.k_new = static_cast<const __nv_bfloat16*>(k_new);
+  p.v_new = static_cast<const __nv_bfloat16*>(v_new);
+  p.k_pages = static_cast<__nv_bfloat16*>(k_pages);
+  p.v_pages = static_cast<__nv_bfloat16*>(v_pages);
+  p.Hq = dims->num_heads_q;
+  p.Hkv = dims->num_heads_kv;
+  p.rotary_dim = rotary_dim;
+  for (int i = 0; i < mimo::kRaMaxHalf; ++i)
+    p.inv_freq[i] = (rotary_dim > 0 && i < rotary_dim / 2)
+                        ? std::pow((double)rope_theta, -2.0 * i / (double)rotary_dim)
+                        : 0.0;
+  mimo::paged_append_kernel<<<total_q, mimo::kPaThreads, 0, (cudaStream_t)stream>>>(p);
+  if ((st = cuda_check(cudaGetLastError(), "paged append launch"))) return st;
+  return ok();
+}
+
+size_t mimo_attn_page_hold_workspace_size(int num_pages) {
+  return num_pages > 0 ? ((size_t)num_pages + 1) * sizeof(int32_t) : 0;
+}
+
+mimo_status_t mimo_attn_page_hold(const int32_t* page_refs, int num_pages, const int32_t* block_table,
+                                  int num_seqs, int max_pages, int page_size, const int32_t* seqlens,
+                                  const int32_t* first, const int32_t* write_from, int32_t* page_refs_out,
+                                  int32_t* block_table_out, int32_t* moves, int32_t* info, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  NvtxRange nvtx_range("mimo_attn_page_hold");
+  mimo_status_t st = check_page_table(page_refs, num_pages, block_table, num_seqs, max_pages, page_refs_out,
+                                      block_table_out);
+  if (st) return st;
+  if (page_size <= 0) return fail(MIMO_ERR_INVALID_ARG, "page_size must be positive (got %d)", page_size);
+  if ((long)max_pages * page_size > 0x7fffffffL)
+    return fail(MIMO_ERR_UNSUPPORTED, "max_pages * page_size must fit in int32");
+  if ((num_seqs > 0 && (!seqlens || !moves)) || !info)
+    return fail(MIMO_ERR_INVALID_ARG, "seqlens, moves and info must be non-NULL");
+  if (!aligned4(seqlens) || !aligned4(first) || !aligned4(write_from) || !aligned4(moves) || !aligned4(info))
+    return fail(MIMO_ERR_INVALID_ARG, "seqlens, first, write_from, moves and info must be 4-byte aligned");
+  const size_t need = mimo_attn_page_hold_workspace_size(num_pages);
+  if (!workspace || workspace_bytes < need || !aligned4(workspace))
+    return fail(MIMO_ERR_WORKSPACE, "workspace of %zu bytes is needed (got %zu)", need,
+                workspace ? workspace_bytes : (size_t)0);
+  mimo::PageHoldParams p;
+  p.refs = page_refs;
+  p.table = block_table;
+  p.seqlens = seqlens;
+  p.first = first;
+  p.write_from = write_from;
+  p.refs_out = page_refs_out;
+  p.table_out = block_table_out;
+  p.moves = moves;
+  p.info = info;
+  p.ws = static_cast<int32_t*>(workspace);
+  p.P = num_pages;
+  p.B = num_seqs;
+  p.M = max_pages;
+  p.page_size = page_size;
+  if ((st = launch_cluster(mimo::page_hold_kernel, p, num_pages + (long)num_seqs * max_pages, stream,
+                           "page hold launch")))
+    return st;
+  return ok();
+}
+
+mimo_status_t mimo_attn_page_fork(const int32_t* page_refs, int num_pages, const int32_t* block_table,
+                                  int num_seqs, int max_pages, const int32_t* parent, int num_seqs_out,
+                                  int32_t* page_refs_out, int32_t* block_table_out, void* stream) {
+  NvtxRange nvtx_range("mimo_attn_page_fork");
+  if (num_seqs_out < 0) return fail(MIMO_ERR_INVALID_ARG, "sizes must be non-negative");
+  // the new table may be empty (everything freed), the old one too
+  const int32_t* out = num_seqs_out > 0 ? block_table_out : block_table;
+  mimo_status_t st = check_page_table(page_refs, num_pages, block_table, num_seqs, max_pages, page_refs_out, out);
+  if (st) return st;
+  if ((long)num_seqs_out * max_pages > 0x7fffffffL)
+    return fail(MIMO_ERR_UNSUPPORTED, "num_seqs_out * max_pages must fit in int32");
+  if (num_seqs_out > 0 && max_pages > 0 && (!parent || !block_table_out || !aligned4(parent) || !aligned4(block_table_out)))
+    return fail(MIMO_ERR_INVALID_ARG, "parent and block_table_out must be non-NULL and 4-byte aligned");
+  if (num_seqs > 0 && num_seqs_out > 0 && max_pages > 0 &&
+      block_table < block_table_out + (size_t)num_seqs_out * max_pages &&
+      block_table_out < block_table + (size_t)num_seqs * max_pages)
+    return fail(MIMO_ERR_INVALID_ARG, "block_table_out must not overlap block_table");
+  mimo::PageForkParams p;
+  p.refs = page_refs;
+  p.table = block_table;
+  p.parent = parent;
+  p.refs_out = page_refs_out;
+  p.table_out = block_table_out;
+  p.P = num_pages;
+  p.B = num_seqs;
+  p.B_out = num_seqs_out;
+  p.M = max_pages;
+  const long elements = num_pages + ((long)num_seqs + num_seqs_out) * max_pages;
+  if ((st = launch_cluster(mimo::page_fork_kernel, p, elements, stream, "page fork launch"))) return st;
+  return ok();
+}
+
+size_t mimo_attn_page_compact_workspace_size(int num_pages) {
+  return num_pages > 0 ? (size_t)num_pages * sizeof(int32_t) : 0;
+}
+
+mimo_status_t mimo_attn_page_compact(const int32_t* page_refs, int num_pages, const int32_t* block_table,
+                                     int num_seqs, int max_pages, int max_moves, int32_t* page_refs_out,
+                                     int32_t* block_table_out, int32_t* moves, int32_t* info, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+  NvtxRange nvtx_range("mimo_attn_page_compact");
+  mimo_status_t st = check_page_table(page_refs, num_pages, block_table, num_seqs, max_pages, page_refs_out,
+                                      block_table_out);
+  if (st) return st;
+  if (max_moves < 0 || max_moves > 0x3fffffff)
+    return fail(MIMO_ERR_INVALID_ARG, "max_moves must be in [0, 2^30) (got %d)", max_moves);
+  if ((max_moves > 0 && !moves) || !info || !aligned4(moves) || !aligned4(info))
+    return fail(MIMO_ERR_INVALID_ARG, "moves and info must be non-NULL and 4-byte aligned");
+  const size_t need = mimo_attn_page_compact_workspace_size(num_pages);
+  if (!workspace || workspace_bytes < need || !aligned4(workspace))
+    return fail(MIMO_ERR_WORKSPACE, "workspace of %zu bytes is needed (got %zu)", need,
+                workspace ? workspace_bytes : (size_t)0);
+  mimo::PageCompactParams p;
+  p.refs = page_refs;
+  p.table = block_table;
+  p.refs_out = page_refs_out;
+  p.table_out = block_table_out;
+  p.moves = moves;
+  p.info = info;
+  p.ws = static_cast<int32_t*>(workspace);
+  p.P = num_pages;
+  p.B = num_seqs;
+  p.M = max_pages;
+  p.max_moves = max_moves;
+  if ((st = launch_cluster(mimo::page_compact_kernel, p, num_pages + (long)num_seqs * max_pages, stream,
+                           "page compact launch")))
+    return st;
+  return ok();
+}
+
+mimo_status_t mimo_attn_page_copy(const mimo_attn_dims_t* dims, void* k_pages, void* v_pages, int num_layers,
+                                  int num_pages, int page_size, const int32_t* moves, int num_moves,
+                                  void* stream) {
+  NvtxRange nvtx_range("mimo_attn_page_copy");
+  mimo_status_t st = check_dims(dims);
+  if (st) return st;
+  if (num_layers < 0 || num_moves < 0) return fail(MIMO_ERR_INVALID_ARG, "sizes must be non-negative");
+  if (num_pages <= 0 || page_size <= 0)
+    return fail(MIMO_ERR_INVALID_ARG, "num_pages and page_size must be positive");
+  const long k_vecs = (long)page_size * dims->num_heads_kv * 24, v_vecs = (long)page_size * dims->num_heads_kv * 16;
+  if (k_vecs > 0x7fffffffL / 2) return fail(MIMO_ERR_UNSUPPORTED, "page_size * num_heads_kv is too large");
+  if (num_layers == 0 || num_moves == 0) return ok();
+  if (!k_pages || !v_pages || !moves) return fail(MIMO_ERR_INVALID_ARG, "k_pages, v_pages and moves must be non-NULL");
+  if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned4(moves))
+    return fail(MIMO_ERR_INVALID_ARG, "k_pages and v_pages must be 16-byte aligned, moves 4-byte");
+  mimo::PageCopyParams p;
+  p.k = static_cast<uint4*>(k_pages);
+  p.v = static_cast<uint4*>(v_pages);
+  p.moves = moves;
+  p.n = num_moves;
+  p.layers = num_layers;
+  p.P = num_pages;
+  p.k_vecs = (int)k_vecs;
+  p.v_vecs = (int)v_vecs;
+  p.k_pieces = (int)((k_vecs + mimo::kPcPiece - 1) / mimo::kPcPiece);
+  p.pieces = p.k_pieces + (int)((v_vecs + mimo::kPcPiece - 1) / mimo::kPcPiece);
+  const double units = (double)num_moves * num_layers * p.pieces;
+  const int grid = (int)std::min<double>(units, 32.0 * sm_count());
+  mimo::page_copy_kernel<<<grid, mimo::kPcThreads, 0, (cudaStream_t)stream>>>(p);
+  if ((st = cuda_check(cudaGetLastError(), "page copy launch"))) return st;
   return ok();
 }
 

@@ -1,0 +1,62 @@
+// What the paged-cache kernels share: the description of a call's sequences
+// and pages, and the checks that keep a bad table or length inside the
+// caller's buffers.
+//
+// A paged cache holds key/value rows in pages of page_size token slots:
+// k_pages [num_pages, page_size, Hkv, 192], v_pages [num_pages, page_size,
+// Hkv, 128].  block_table [num_seqs, max_pages] names the page of each run of
+// page_size positions of a sequence; a negative entry is "no page".  A call
+// brings n_b = cu_q[b+1] - cu_q[b] new tokens of sequence b, packed, which sit
+// at positions L_b - n_b .. L_b - 1 (L_b = seqlens[b], the new tokens included).
+#pragma once
+
+#include "common.cuh"
+
+namespace mimo {
+
+struct PagedBatch {
+  const int32_t* table;    // [num_seqs, max_pages]
+  const int32_t* cu_q;     // [num_seqs + 1]
+  const int32_t* seqlens;  // [num_seqs]
+  int num_seqs, total_q;
+  int max_q;               // >= every n_b
+  int num_pages, page_size, max_pages;
+};
+
+// One sequence of a call: its first packed row, new tokens and length.
+struct PagedSeq {
+  int b0, n, len;
+  bool ok;  // false: an argument of this sequence is out of range, nothing of it is read or written
+};
+
+__device__ __forceinline__ PagedSeq paged_seq(const PagedBatch& p, int b) {
+  PagedSeq s;
+  s.b0 = p.cu_q[b];
+  s.n = p.cu_q[b + 1] - s.b0;
+  s.len = p.seqlens[b];
+  s.ok = seq_in_bounds(s.b0, s.n, p.max_q, p.total_q) && s.n <= s.len &&
+         s.len <= (long long)p.max_pages * p.page_size;
+  return s;
+}
+
+// The sequence of packed row t: the last b with cu_q[b] <= t among those that
+// have rows (upper bound of t in cu_q, less one); -1 for a row that none owns.
+__device__ __forceinline__ int paged_seq_of_row(const PagedBatch& p, int t) {
+  int lo = 0, hi = p.num_seqs;  // cu_q[lo] <= t < cu_q[hi] for a sound cu_q
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (p.cu_q[mid + 1] <= t) lo = mid + 1; else hi = mid;
+  }
+  return (lo < p.num_seqs && p.cu_q[lo] <= t) ? lo : -1;
+}
+
+// The page that holds positions [j * page_size, (j + 1) * page_size) of
+// sequence b; -1 (recorded as MIMO_ERR_INVALID_ARG) where the table names none.
+__device__ __forceinline__ int paged_page(const PagedBatch& p, int b, int j) {
+  const int e = p.table[(size_t)b * p.max_pages + j];
+  if (e >= 0 && e < p.num_pages) return e;
+  record_status(1 /* MIMO_ERR_INVALID_ARG */);
+  return -1;
+}
+
+}  // namespace mimo

@@ -312,6 +312,163 @@ mimo_status_t mimo_attn_decode_noalloc(const mimo_attn_dims_t* dims, const void*
                                        int window, const float* sinks, void* out,
                                        float* lse, void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Paged cache.
+ *
+ * The keys and values of a layer sit in pages of page_size token slots, any
+ * page holding any run of page_size positions of any sequence (the caller of
+ * MiMoV2FlashModel.forward passes only the unprocessed tokens; their cache is
+ * past_key_values):
+ *
+ *   k_pages      [num_pages, page_size, Hkv, Dqk] bf16
+ *   v_pages      [num_pages, page_size, Hkv, Dv ] bf16
+ *   block_table  [num_seqs, max_pages] int32 on the device: entry j names the
+ *                page of positions [j*page_size, (j+1)*page_size); a negative
+ *                entry is "no page"
+ *   seqlens      [num_seqs] int32 on the device: tokens so far INCLUDING the new ones
+ *   cu_seqlens_q [num_seqs+1] int32 on the device, non-decreasing from 0: the
+ *                n_b = cu[b+1] - cu[b] >= 0 new tokens of sequence b are the packed
+ *                rows [cu[b], cu[b+1]), at positions seqlens[b] - n_b .. seqlens[b] - 1
+ *   page_refs    [num_pages] int32 on the device: how many block_table entries
+ *                name each page; 0 = free
+ *
+ * page_size is a multiple of 16 for the calls that read or write keys and
+ * values (else MIMO_ERR_UNSUPPORTED); num_pages * page_size and max_pages *
+ * page_size fit in int32.  Packed rows from cu[num_seqs] on (up to total_q)
+ * belong to no sequence: their outputs are left as they were.
+ *
+ * A sequence with n_b < 0, rows outside [0, total_q), n_b > max_seqlen_q, n_b >
+ * seqlens[b] or seqlens[b] > max_pages * page_size is skipped (nothing of it is
+ * written) and recorded as MIMO_ERR_INVALID_ARG in the device status word.  A
+ * table entry that is needed and names no page below num_pages is recorded the
+ * same way; no memory outside the pages is touched (see each call).
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Bytes of device workspace mimo_attn_paged_attention needs for these sizes.
+ */
+size_t mimo_attn_paged_attention_workspace_size(const mimo_attn_dims_t* dims, int num_seqs, int total_q,
+                                                int max_seqlen_q);
+
+/*
+ * Attention of the new tokens over the paged cache, which already holds their
+ * own keys and values: chunked prefill (n_b large), checking of drafted tokens
+ * (n_b a handful) and decode (n_b = 1), in one batch if need be.  The formula is
+ * that of mimo_attn_prefill with query row i of sequence b at position
+ * p = seqlens[b] - n_b + i: keys j with 0 <= p - j, and p - j <= window - 1 if
+ * window > 0.
+ *
+ *   q            [total_q, Hq, Dqk] bf16, post-RoPE
+ *   max_seqlen_q >= every n_b (not read back from the device)
+ *   window       0 = global; >= 1 = the query plus window-1 earlier keys
+ *   sinks        [Hq] fp32 or NULL
+ *   out          [total_q, Hq, Dv] in dims->out_dtype
+ *   lse          [Hq, total_q] fp32 or NULL
+ *   workspace    >= mimo_attn_paged_attention_workspace_size() bytes, 16-byte
+ *                aligned (may be NULL when that size is 0); its contents need no
+ *                preparation.  Calls sharing one workspace must not overlap on the GPU.
+ *
+ * Hq / Hkv <= 128.  Slots that no query of the sequence sees (past its length,
+ * behind its window) may hold anything, NaN included, and their table entries
+ * may be negative: they are not read into the result.  A key or value that some
+ * queries of the chunk see and others do not must be finite.  A visible entry
+ * without a page reads as zero keys and values.
+ */
+mimo_status_t mimo_attn_paged_attention(const mimo_attn_dims_t* dims, const void* q, const void* k_pages,
+                                        const void* v_pages, const int32_t* block_table,
+                                        const int32_t* cu_seqlens_q, const int32_t* seqlens, int num_seqs,
+                                        int total_q, int max_seqlen_q, int num_pages, int page_size,
+                                        int max_pages, int window, const float* sinks, void* out, float* lse,
+                                        void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The rotation of the new tokens' queries and keys and the write of their keys
+ * and values into the pages (run before mimo_attn_paged_attention on the same
+ * stream): mimo_attn_rope_append for a chunk and a paged cache, with the same
+ * rotation, rope_theta and rotary_dim.
+ *
+ *   q       [total_q, Hq, Dqk] bf16;  q_out: the rotated queries, same shape
+ *           (may be q itself; must not overlap it otherwise)
+ *   k_new   [total_q, Hkv, Dqk] bf16 before rotation;  v_new [total_q, Hkv, Dv] bf16
+ *
+ * Only the slots of the new positions are written.  A position without a page
+ * is recorded as MIMO_ERR_INVALID_ARG: its query is rotated, its key and value
+ * are not stored.
+ */
+mimo_status_t mimo_attn_paged_append(const mimo_attn_dims_t* dims, const void* q, void* q_out,
+                                     const void* k_new, const void* v_new, void* k_pages, void* v_pages,
+                                     const int32_t* block_table, const int32_t* cu_seqlens_q,
+                                     const int32_t* seqlens, int num_seqs, int total_q, int num_pages,
+                                     int page_size, int max_pages, float rope_theta, int rotary_dim,
+                                     void* stream);
+
+/*
+ * Page bookkeeping, wholly on the device (nothing is read back, so the calls can
+ * be captured in a graph).  page_refs_out may be page_refs and, but for fork,
+ * block_table_out may be block_table (in place); otherwise the outputs must
+ * not overlap the inputs.  Results are deterministic.  block_table entries at
+ * or above num_pages are recorded as MIMO_ERR_INVALID_ARG and count as no page
+ * (fork and compact pass them on), as is a held page whose count is not positive.
+ *
+ * mimo_attn_page_hold: afterwards sequence b holds the pages of entries
+ * first[b] / page_size .. ceil(seqlens[b] / page_size) - 1 and no others.
+ *   first      [num_seqs] int32 or NULL (0): the first position still needed (a
+ *              sliding window leaves pages behind)
+ *   write_from [num_seqs] int32 or NULL: positions from here on will be written,
+ *              so an entry that reaches past it and whose page others hold too
+ *              (page_refs > 1 once this call's releases are counted) gets a page
+ *              of its own; where the old page also holds positions below
+ *              write_from, `moves` asks for its copy
+ *   moves      [num_seqs, 2] int32: (source page, destination page) to copy with
+ *              mimo_attn_page_copy before anything is written, or (-1, -1)
+ *   info       [2] int32: pages that were missing, pages free afterwards
+ * Releases come first; then the entries that need a page get the free pages,
+ * lowest index first, in order of (sequence, entry).  If they do not suffice,
+ * info[0] > 0 says by how many and nothing else changes (counts and table are
+ * as before, no moves).  A sequence with a negative seqlens, first or write_from,
+ * or seqlens > max_pages * page_size, keeps its pages as they are and is recorded
+ * as MIMO_ERR_INVALID_ARG.
+ *
+ * mimo_attn_page_fork: row i of block_table_out [num_seqs_out, max_pages] is row
+ * parent[i] of block_table (empty where parent[i] < 0): forks, beam reordering
+ * and ended sequences in one call.  Pages that no row names any more become
+ * free.  parent[i] >= num_seqs is recorded as MIMO_ERR_INVALID_ARG (an empty row).
+ *
+ * mimo_attn_page_compact: with u pages in use, moves the k-th used page at or
+ * above u to the k-th free page below it, for the first max_moves of them.
+ *   moves      [max_moves, 2] int32: the copies to make, then (-1, -1)
+ *   info       [2] int32: moves made, pages in use
+ */
+size_t mimo_attn_page_hold_workspace_size(int num_pages);
+mimo_status_t mimo_attn_page_hold(const int32_t* page_refs, int num_pages, const int32_t* block_table,
+                                  int num_seqs, int max_pages, int page_size, const int32_t* seqlens,
+                                  const int32_t* first, const int32_t* write_from, int32_t* page_refs_out,
+                                  int32_t* block_table_out, int32_t* moves, int32_t* info, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+mimo_status_t mimo_attn_page_fork(const int32_t* page_refs, int num_pages, const int32_t* block_table,
+                                  int num_seqs, int max_pages, const int32_t* parent, int num_seqs_out,
+                                  int32_t* page_refs_out, int32_t* block_table_out, void* stream);
+size_t mimo_attn_page_compact_workspace_size(int num_pages);
+mimo_status_t mimo_attn_page_compact(const int32_t* page_refs, int num_pages, const int32_t* block_table,
+                                     int num_seqs, int max_pages, int max_moves, int32_t* page_refs_out,
+                                     int32_t* block_table_out, int32_t* moves, int32_t* info, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
+/*
+ * Copies whole pages, moves[m] = (source, destination), in each of num_layers
+ * layers: k_pages [num_layers, num_pages, page_size, Hkv, Dqk] and v_pages
+ * [num_layers, num_pages, page_size, Hkv, Dv] bf16.  Of dims, num_heads_kv and the
+ * head dimensions matter.  Rows (-1, -1) are skipped; a row with one page out of
+ * range is skipped and recorded as MIMO_ERR_INVALID_ARG.  The copies happen in
+ * no order: a destination must not be named twice nor be a source (the moves
+ * of mimo_attn_page_hold and mimo_attn_page_compact never are).
+ */
+mimo_status_t mimo_attn_page_copy(const mimo_attn_dims_t* dims, void* k_pages, void* v_pages, int num_layers,
+                                  int num_pages, int page_size, const int32_t* moves, int num_moves,
+                                  void* stream);
+
 /* Message for the calling thread's last non-OK status ("" if none). */
 const char* mimo_attn_last_error(void);
 

@@ -18,6 +18,8 @@ Modules
 ``fp8``        e4m3 decoding from the format's definition and decode over FP8
                KV caches with per-KV-head scales (``attention.decode`` on the
                dequantised caches).
+``paged``      attention, rotation and write of a chunk of tokens over a paged
+               cache, and the page bookkeeping, one row and one entry at a time.
 ``backward``   gradients of the prefill (q, k, v and the sink logits) from
                explicit probability matrices, pinned to finite differences;
                ``prefill_backward_sampled`` gives them at chosen positions of

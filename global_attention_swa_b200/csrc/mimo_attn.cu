@@ -922,6 +922,44 @@ mimo::PagedBatch paged_batch(const int32_t* block_table, const int32_t* cu_seqle
   return b;
 }
 
+// Workspace of the paged attention: a descriptor per CTA and two slots of
+// partial results, tiles * 128 rows each (offsets from a 32-byte boundary).
+struct PagedWorkspace {
+  size_t off_ml, off_o, bytes;
+};
+PagedWorkspace paged_workspace(int tiles) {
+  PagedWorkspace w;
+  const size_t ctas = sm_count(), rows = ctas * 2 * tiles * 128;
+  w.off_ml = (ctas * sizeof(mimo::PgDesc) + 31) / 32 * 32;
+  w.off_o = w.off_ml + rows * sizeof(float4);
+  w.bytes = w.off_o + rows * 128 * sizeof(float) + 32;
+  return w;
+}
+
+// Every sequence's new tokens fit one tile of rows.
+bool paged_one_tile(const mimo_attn_dims_t* dims, int max_seqlen_q) {
+  return max_seqlen_q <= 128 / (dims->num_heads_q / dims->num_heads_kv);
+}
+
+// Opt the paged attention into its dynamic shared memory once per device.
+mimo_status_t ensure_paged_attributes() {
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return fail(MIMO_ERR_CUDA, "cudaGetDevice failed");
+  if (done[dev].load(std::memory_order_acquire)) return MIMO_OK;
+  mimo_status_t st;
+  if ((st = cuda_check(cudaFuncSetAttribute(mimo::paged_attention_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            mimo::PgLayout<1>::kSmemBytes),
+                       "paged attention smem attribute")))
+    return st;
+  if ((st = cuda_check(cudaFuncSetAttribute(mimo::paged_attention_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            mimo::PgLayout<2>::kSmemBytes),
+                       "paged attention smem attribute")))
+    return st;
+  done[dev].store(true, std::memory_order_release);
+  return MIMO_OK;
+}
+
 // The arrays of the page bookkeeping calls.
 mimo_status_t check_page_table(const int32_t* page_refs, int num_pages, const int32_t* block_table,
                                int num_seqs, int max_pages, const int32_t* refs_out, const int32_t* table_out) {
@@ -963,11 +1001,10 @@ extern "C" {
 
 size_t mimo_attn_paged_attention_workspace_size(const mimo_attn_dims_t* dims, int num_seqs, int total_q,
                                                 int max_seqlen_q) {
-  (void)dims;
-  (void)num_seqs;
-  (void)total_q;
-  (void)max_seqlen_q;
-  return 0;
+  if (!dims || dims->num_heads_q <= 0 || dims->num_heads_kv <= 0 || num_seqs <= 0 || total_q <= 0 ||
+      max_seqlen_q <= 0 || dims->num_heads_q / dims->num_heads_kv > 128)
+    return 0;
+  return paged_workspace(paged_one_tile(dims, max_seqlen_q) ? 1 : 2).bytes;
 }
 
 mimo_status_t mimo_attn_paged_attention(const mimo_attn_dims_t* dims, const void* q, const void* k_pages,
@@ -991,29 +1028,82 @@ mimo_status_t mimo_attn_paged_attention(const mimo_attn_dims_t* dims, const void
   if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) || !aligned4(lse) ||
       !aligned4(sinks))
     return fail(MIMO_ERR_INVALID_ARG, "q, k_pages, v_pages and out must be 16-byte aligned");
-  const size_t need = mimo_attn_paged_attention_workspace_size(dims, num_seqs, total_q, max_seqlen_q);
-  if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
-    return fail(MIMO_ERR_WORKSPACE, "workspace of %zu bytes, 16-byte aligned, is needed (got %zu)", need,
+  const int tiles = paged_one_tile(dims, max_seqlen_q) ? 1 : 2;
+  const PagedWorkspace ws = paged_workspace(tiles);
+  if (!workspace || workspace_bytes < ws.bytes || !aligned16(workspace))
+    return fail(MIMO_ERR_WORKSPACE, "workspace of %zu bytes, 16-byte aligned, is needed (got %zu)", ws.bytes,
                 workspace ? workspace_bytes : (size_t)0);
+  if ((st = ensure_paged_attributes())) return st;
+
   mimo::PagedAttnParams p;
   p.pb = paged_batch(block_table, cu_seqlens_q, seqlens, num_seqs, total_q, max_seqlen_q, num_pages, page_size,
                      max_pages);
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.k = static_cast<const __nv_bfloat16*>(k_pages);
-  p.v = static_cast<const __nv_bfloat16*>(v_pages);
   p.sinks = sinks;
   p.out = out;
   p.lse = lse;
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(workspace) + 31) & ~uintptr_t(31));
+  p.ws_desc = reinterpret_cast<mimo::PgDesc*>(base);
+  p.ws_ml = reinterpret_cast<float4*>(base + ws.off_ml);
+  p.ws_o = reinterpret_cast<float*>(base + ws.off_o);
   p.Hq = Hq;
   p.Hkv = Hkv;
   p.G = G;
+  p.TQ = 128 / G;
   p.window = window;
+  // Boxes: as many keys as divide both a page and a tile.  Under a short window
+  // 16, so that an item reads few keys more than it sees.
+  int box = 128;
+  while (page_size % box) box /= 2;
+  if (window > 0 && window <= 512) box = 16;
+  p.box_rows = box;
+  // With at most four key tiles to an item, only whole items are dealt out:
+  // joining parts would cost more than the shares' imbalance.
+  const int D = tiles * p.TQ;
+  p.split = !(window > 0 && (window - 1L + D + box - 1 + 127) / 128 <= 4);
+  p.min_tiles = 2;
   p.scale_log2 = scale_log2_of(dims);
   p.v_scale = v_scale_of(dims);
   p.out_f32 = dims->out_dtype == MIMO_DTYPE_F32;
-  const long blocks = ((long)total_q * Hq + 7) / 8;
-  mimo::paged_attention_kernel<<<(int)std::min<long>(blocks, 8L * sm_count()), 256, 0, (cudaStream_t)stream>>>(p);
+  p.out_v8 = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
+
+  CUtensorMap tq, tk, tv;
+  {
+    const uint64_t d[3] = {192, (uint64_t)Hq, (uint64_t)total_q};
+    const uint64_t s[2] = {192 * 2, (uint64_t)Hq * 192 * 2};
+    const uint32_t b[3] = {64, (uint32_t)G, (uint32_t)p.TQ};
+    if ((st = make_map(&tq, q, 3, d, s, b))) return st;
+  }
+  {
+    const uint64_t d[3] = {192, (uint64_t)Hkv, (uint64_t)num_pages * page_size};
+    const uint64_t s[2] = {192 * 2, (uint64_t)Hkv * 192 * 2};
+    const uint32_t b[3] = {64, 1, (uint32_t)box};
+    if ((st = make_map(&tk, k_pages, 3, d, s, b))) return st;
+  }
+  {
+    const uint64_t d[3] = {128, (uint64_t)Hkv, (uint64_t)num_pages * page_size};
+    const uint64_t s[2] = {128 * 2, (uint64_t)Hkv * 128 * 2};
+    const uint32_t b[3] = {64, 1, (uint32_t)box};
+    if ((st = make_map(&tv, v_pages, 3, d, s, b))) return st;
+  }
+  // no more CTAs than items when only whole ones are dealt out; there are at
+  // most total_q / D + num_seqs blocks
+  const int ctas = p.split ? sm_count()
+                           : (int)std::min<long>(sm_count(), ((long)total_q / D + num_seqs) * Hkv);
+  if (tiles == 1)
+    mimo::paged_attention_kernel<1><<<ctas, mimo::kPgThreads, mimo::PgLayout<1>::kSmemBytes, (cudaStream_t)stream>>>(
+        tq, tk, tv, p);
+  else
+    mimo::paged_attention_kernel<2><<<ctas, mimo::kPgThreads, mimo::PgLayout<2>::kSmemBytes, (cudaStream_t)stream>>>(
+        tq, tk, tv, p);
   if ((st = cuda_check(cudaGetLastError(), "paged attention launch"))) return st;
+  if (p.split) {
+    const dim3 grid(ctas, tiles == 1 ? 4 : 8);
+    if (tiles == 1)
+      mimo::paged_combine_kernel<1><<<grid, 256, 0, (cudaStream_t)stream>>>(p);
+    else
+      mimo::paged_combine_kernel<2><<<grid, 256, 0, (cudaStream_t)stream>>>(p);
+    if ((st = cuda_check(cudaGetLastError(), "paged combine launch"))) return st;
+  }
   return ok();
 }
 

@@ -1,12 +1,41 @@
-// Attention of a chunk of new tokens over a paged cache.
+// Attention of a chunk of new tokens over a paged cache, on 5th-generation
+// tensor cores (tcgen05).
 //
 // Row (token i of the chunk, query head h) at position p = L - n + i sees the
 // keys j with 0 <= p - j and, in a window, p - j <= window - 1:
 //   m = max(sigma_h, max_j S_j),  Z = exp(sigma_h - m) + sum_j exp(S_j - m),
 //   out = v_scale * sum_j exp(S_j - m) v_j / Z,  lse = m + ln Z.
 //
-// One warp per row: a lane holds 6 of the 192 query dimensions and 4 of the
-// 128 value columns, and the keys pass one at a time through an online softmax.
+// A tile is the G query heads of one key/value head x TQ = 128 / G tokens: its
+// 128 rows share every key and value they read.  An item is one key/value
+// head x kTiles tiles of consecutive tokens of a sequence; its keys pass in
+// tiles of 128 through shared memory, each feeding kTiles score products.
+//
+// Work is dealt out in keys, not in items.  All items laid end to end (by
+// sequence, key/value head, token block) are cut into equal shares, one per
+// CTA, wherever the cut falls; an item that a cut divides leaves its parts
+// (unnormalised O, reference m, sums l) in the workspace, and
+// paged_combine_kernel joins them.  Lengths are read on the device: every CTA
+// finds its own share from them.  With short windows an item is a tile or two
+// and only whole items are dealt out.
+//
+//   warp 8      loads Q and K (TMA), allocates TMEM
+//   warp 9      issues the MMAs (one thread): S = Q K^T (SS), O += P V (TS, P from TMEM)
+//   warp 10     loads V (TMA)
+//   warp 11     zeroes the value rows of a key tile that the item does not see
+//               (they may hold anything, and 0 * NaN would reach the sum)
+//   warps 0-3   softmax and epilogue of tile 0 (one row per thread)
+//   warps 4-7   softmax and epilogue of tile 1
+//
+// The page table is looked up by the loading warps, one lane per box of
+// box_rows keys (a divisor of the page size): a key tile may span many pages
+// or part of one.  An entry that names no page is loaded from past the end of
+// the pool, which the TMA unit fills with zeros.
+//
+// Softmax as in prefill_kernel: base 2, against a reference m that moves only
+// when a tile's sum would leave the safe range; P is rounded to bf16 for the
+// P.V product (the tensor cores take 16-bit operands beside bf16 V) and the
+// output is normalised by the sum of the rounded values; l, m and O are fp32.
 #pragma once
 
 #include "paged_common.cuh"
@@ -16,74 +45,818 @@
 
 namespace mimo {
 
+constexpr int kPgThreads = 384;
+constexpr int kPgKeys = 128;                 // keys of a tile
+constexpr int kPgQBytes = 128 * 192 * 2;     // 3 boxes of [128 rows][64 dims]
+constexpr int kPgKBytes = kPgKeys * 192 * 2;
+constexpr int kPgVBytes = kPgKeys * 128 * 2;
+constexpr int kPgKStages = 2;
+
+// Two tiles share a key tile: Q 2 x 48 KB, K 2 x 48 KB, V 32 KB.  One tile (a
+// handful of new tokens: bound by the cache's bytes): V has two stages too.
+template <int kTiles>
+struct PgLayout {
+  static constexpr int kVStages = kTiles == 1 ? 2 : 1;
+  static constexpr int kOffK = kTiles * kPgQBytes;
+  static constexpr int kOffV = kOffK + kPgKStages * kPgKBytes;
+  static constexpr int kOffBar = kOffV + kVStages * kPgVBytes;
+  static constexpr int kSmemBytes = kOffBar + 512 + 1024;  // barriers, plan; alignment slack
+};
+
+// Partial results in the workspace: one descriptor per CTA, then for each CTA
+// two slots (0: the item its share begins inside of, 1: the item its share
+// ends inside of) of kTiles * 128 rows.
+struct PgDesc {
+  int open0;    // slot 0 holds a part: 1, and 2 if the item ends there
+  int open1;    // slot 1 holds the first part of an item
+  int row0;     // slot 1's item: first packed row (token)
+  int h0;       //   first query head
+  int rows;     //   valid rows (tokens * G)
+  int pad[3];
+};
+
 struct PagedAttnParams {
   PagedBatch pb;
-  const __nv_bfloat16* q;  // [total_q, Hq, 192]
-  const __nv_bfloat16* k;  // [num_pages, page_size, Hkv, 192]
-  const __nv_bfloat16* v;  // [num_pages, page_size, Hkv, 128]
   const float* sinks;      // [Hq] or null
   void* out;               // [total_q, Hq, 128]
   float* lse;              // [Hq, total_q] or null
+  PgDesc* ws_desc;         // [ctas]
+  float4* ws_ml;           // [ctas, 2, kTiles * 128]: m, l, sum of the rounded P
+  float* ws_o;             // [ctas, 2, kTiles * 128, 128]
   int Hq, Hkv, G;
+  int TQ;                  // tokens of a tile: 128 / G
   int window;
+  int box_rows;            // keys of one TMA box; divides page_size and 128
+  int split;               // 1: cut items anywhere, 0: deal out whole items
+  int min_tiles;           // smallest share, in key tiles
   float scale_log2, v_scale;
   int out_f32;
+  int out_v8;              // out is 32-byte aligned
 };
 
-__global__ void __launch_bounds__(256) paged_attention_kernel(const PagedAttnParams p) {
-  const int lane = threadIdx.x & 31;
-  const long long rows = (long long)p.pb.total_q * p.Hq;
-  for (long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); w < rows; w += (long long)gridDim.x * 8) {
-    const int t = (int)(w / p.Hq), h = (int)(w % p.Hq), g = h / p.G;
-    const int b = paged_seq_of_row(p.pb, t);
-    if (b < 0) continue;
-    const PagedSeq s = paged_seq(p.pb, b);
-    if (!s.ok || t < s.b0 || t >= s.b0 + s.n) {
-      if (!s.ok) record_status(1 /* MIMO_ERR_INVALID_ARG */);
-      continue;
+// A place in the list of all items: an item, and a key tile of it.
+struct PgPlace {
+  int b, g, i, t;
+};
+
+// Cost of an item of a sequence, in keys: what it reads.  In a window that is
+// the same for all blocks; without one, block i reads first + D (i + 1) keys
+// (first: the position of the chunk's first token, D: tokens of a block).
+// With whole items only, 1.
+struct PgCost {
+  long long base;  // block 0
+  int slope;       // each further block
+  int blocks;
+  __device__ __forceinline__ long long upto(int i) const {  // blocks 0 .. i-1
+    return base * i + (long long)slope * ((long long)i * (i - 1) / 2);
+  }
+  // the block that holds cost y of [0, upto(blocks))
+  __device__ __forceinline__ int block_of(long long y) const {
+    int i;
+    if (slope == 0) {
+      i = (int)(y / base);
+    } else {
+      const double h = (double)base - 0.5 * slope;
+      i = (int)((sqrt(h * h + 2.0 * slope * (double)y) - h) / slope);
     }
-    const int pos = s.len - s.n + (t - s.b0);
-    const int lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
-    float2 q[3];
-#pragma unroll
-    for (int c = 0; c < 3; ++c)
-      q[c] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p.q + w * 192 + 64 * c + 2 * lane));
-    float m = p.sinks ? p.sinks[h] * 1.4426950408889634f : -INFINITY;
-    float l = p.sinks ? 1.f : 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    int page = -1;
-    for (int j = lo; j <= pos; ++j) {
-      const int slot = j % p.pb.page_size;
-      if (j == lo || slot == 0) page = paged_page(p.pb, b, j / p.pb.page_size);
-      float x = 0.f;  // a key without a page reads as zeros
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      const long long row = ((long long)page * p.pb.page_size + slot) * p.Hkv + g;
-      if (page >= 0 && MIMO_ROW_OK(row, (long long)p.pb.num_pages * p.pb.page_size * p.Hkv)) {
-#pragma unroll
-        for (int c = 0; c < 3; ++c) {
-          const float2 k = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p.k + row * 192 + 64 * c + 2 * lane));
-          x += q[c].x * k.x + q[c].y * k.y;
+    i = max(0, min(i, blocks - 1));
+    while (i > 0 && upto(i) > y) --i;
+    while (i + 1 < blocks && upto(i + 1) <= y) ++i;
+    return i;
+  }
+};
+template <int kTiles>
+__device__ __forceinline__ PgCost pg_cost(const PagedAttnParams& p, const PagedSeq& s) {
+  PgCost c;
+  const int D = kTiles * p.TQ;
+  c.blocks = s.ok ? (s.n + D - 1) / D : 0;
+  if (!p.split) {
+    c.base = 1;
+    c.slope = 0;
+  } else if (p.window > 0) {
+    c.base = (long long)p.window + D;
+    c.slope = 0;
+  } else {
+    c.base = (long long)(s.len - s.n) + D;
+    c.slope = D;
+  }
+  return c;
+}
+
+// One item as a role sees it: its keys and the tiles of them in this share.
+struct PgItem {
+  int b, g, i;      // sequence, key/value head, block
+  int tok0;         // packed row of its first token
+  int p0;           // that token's position
+  int tokens;       // valid tokens, 1 .. kTiles * TQ
+  int lo, hi;       // keys that some row sees: [lo, hi]
+  int start;        // first key of tile 0: lo rounded down to a box
+  int n_kt;         // key tiles
+  int t0, t1;       // the tiles of this share
+};
+
+// Walks the items of a share.
+template <int kTiles>
+struct PgWalk {
+  PgPlace at, end;
+  PagedSeq s;
+  int blocks;
+  bool first;
+  __device__ __forceinline__ void seq(const PagedAttnParams& p) {
+    const int D = kTiles * p.TQ;
+    blocks = 0;
+    while (at.b < p.pb.num_seqs) {
+      s = paged_seq(p.pb, at.b);
+      blocks = s.ok ? (s.n + D - 1) / D : 0;
+      if (blocks > 0) break;
+      ++at.b;
+    }
+  }
+  __device__ __forceinline__ PgWalk(const PagedAttnParams& p, const PgPlace* plan) : at(plan[0]), end(plan[1]), first(true) {
+    seq(p);
+  }
+  // The next item with work in this share; false at its end.
+  __device__ __forceinline__ bool next(const PagedAttnParams& p, PgItem& it) {
+    while (true) {
+      if (!first) {  // past the item of the last call
+        if (at.b == end.b && at.g == end.g && at.i == end.i) return false;
+        at.t = 0;
+        if (++at.i >= blocks) {
+          at.i = 0;
+          if (++at.g >= p.Hkv) {
+            at.g = 0;
+            ++at.b;
+            seq(p);
+          }
         }
-        const uint2 u = *reinterpret_cast<const uint2*>(p.v + row * 128 + 4 * lane);
-        v = make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
       }
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-      x *= p.scale_log2;
-      const float mn = fmaxf(m, x);
-      const float a = (m == -INFINITY) ? 0.f : ex2(m - mn), e = ex2(x - mn);
-      m = mn;
-      l = l * a + e;
-      o = make_float4(o.x * a + e * v.x, o.y * a + e * v.y, o.z * a + e * v.z, o.w * a + e * v.w);
+      first = false;
+      const bool last = at.b == end.b && at.g == end.g && at.i == end.i;
+      if (at.b >= p.pb.num_seqs || (last && end.t == 0)) return false;
+      const int D = kTiles * p.TQ;
+      it.b = at.b;
+      it.g = at.g;
+      it.i = at.i;
+      it.tok0 = s.b0 + at.i * D;
+      it.p0 = s.len - s.n + at.i * D;
+      it.tokens = min(D, s.n - at.i * D);
+      it.hi = it.p0 + it.tokens - 1;
+      it.lo = p.window > 0 ? max(0, it.p0 - p.window + 1) : 0;
+      it.start = it.lo / p.box_rows * p.box_rows;
+      it.n_kt = (it.hi - it.start) / kPgKeys + 1;
+      it.t0 = at.t;
+      it.t1 = last ? min(end.t, it.n_kt) : it.n_kt;
+      if (it.t0 < it.t1) return true;
     }
-    if (!MIMO_ROW_OK(w, rows)) continue;
-    const float f = l > 0.f ? p.v_scale / l : 0.f;
+  }
+};
+
+// Key tile t of an item: its first key, how many the products take (a multiple
+// of 16), and the rows [0, zlo) and [zhi, n) that nothing of the item sees.
+struct PgTile {
+  int k0, n, zlo, zhi;
+};
+__device__ __forceinline__ PgTile pg_tile(const PgItem& it, int t) {
+  PgTile r;
+  r.k0 = it.start + t * kPgKeys;
+  const int left = it.hi + 1 - r.k0;
+  r.n = min(kPgKeys, (left + 15) & ~15);
+  r.zlo = max(0, it.lo - r.k0);
+  r.zhi = min(r.n, left);
+  return r;
+}
+
+// This CTA's share.  All threads call it; plan (shared) holds the first place
+// and the one past the last afterwards.  Returns false where there is no share.
+template <int kTiles>
+__device__ __forceinline__ bool pg_plan(const PagedAttnParams& p, PgPlace* plan, long long* warp_sum) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int each = (p.pb.num_seqs + kPgThreads - 1) / kPgThreads;
+  const int b0 = threadIdx.x * each, b1 = min(p.pb.num_seqs, b0 + each);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    const PagedSeq s = paged_seq(p.pb, b);
+    if (!s.ok && blockIdx.x == 0) record_status(1 /* MIMO_ERR_INVALID_ARG */);
+    const PgCost c = pg_cost<kTiles>(p, s);
+    mine += c.upto(c.blocks) * p.Hkv;
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += x;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  if (threadIdx.x == 0) plan[0] = plan[1] = PgPlace{p.pb.num_seqs, 0, 0, 0};
+  __syncthreads();
+  long long before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < kPgThreads / 32; ++w) {
+    const long long x = warp_sum[w];
+    if (w < warp) before += x;
+    total += x;
+  }
+  before += incl - mine;
+  const long long unit = p.split ? (long long)kPgKeys * p.min_tiles : 1;
+  const long long shares = max(1LL, min((long long)gridDim.x, total / unit));
+  const int c = blockIdx.x;
+#pragma unroll 1
+  for (int k = 0; k < 2; ++k) {
+    const long long x = total * min((long long)c + k, shares) / shares;
+    if (x < before || x >= before + mine) continue;
+    long long y = x - before;
+    for (int b = b0; b < b1; ++b) {
+      const PgCost cost = pg_cost<kTiles>(p, paged_seq(p.pb, b));
+      const long long group = cost.upto(cost.blocks), all = group * p.Hkv;
+      if (y >= all) {
+        y -= all;
+        continue;
+      }
+      PgPlace pl;
+      pl.b = b;
+      pl.g = (int)(y / group);
+      y -= pl.g * group;
+      pl.i = cost.block_of(y);
+      pl.t = p.split ? (int)((y - cost.upto(pl.i)) / kPgKeys) : 0;
+      plan[k] = pl;
+      break;
+    }
+  }
+  __syncthreads();
+  return c < shares && total > 0;
+}
+
+// The pool row (page * page_size + slot) at which box j of a tile begins; past
+// the pool's end, where the loads read zeros, for an entry that names no page.
+__device__ __forceinline__ int pg_box_row(const PagedAttnParams& p, const PgItem& it, const PgTile& tl, int j) {
+  const int pos = tl.k0 + j * p.box_rows;
+  const int page = pos / p.pb.page_size;
+  int e = -1;
+  if (MIMO_ROW_OK((long long)it.b * p.pb.max_pages + page, (long long)p.pb.num_seqs * p.pb.max_pages))
+    e = paged_page(p.pb, it.b, page);
+  return e < 0 ? p.pb.num_pages * p.pb.page_size : e * p.pb.page_size + (pos - page * p.pb.page_size);
+}
+
+template <int kTiles>
+__global__ void __launch_bounds__(kPgThreads, 1)
+    paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                           const __grid_constant__ CUtensorMap tm_v, const PagedAttnParams p) {
+  using Lay = PgLayout<kTiles>;
+  constexpr int kVStages = Lay::kVStages;
+  extern __shared__ __align__(1024) uint8_t pgsmem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(pgsmem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::kOffBar);
+  uint64_t* q_full = bars + 0;
+  uint64_t* q_empty = bars + 1;
+  uint64_t* k_full = bars + 2;    // [2]
+  uint64_t* k_empty = bars + 4;   // [2]
+  uint64_t* v_full = bars + 6;    // [kVStages]
+  uint64_t* v_empty = bars + 8;   // [kVStages]
+  uint64_t* v_ready = bars + 10;  // [kVStages] once warp 11 has zeroed a tile's unseen rows
+  uint64_t* s_full = bars + 12;   // [2] two tiles: of tile i; one: of key tile parity i
+  uint64_t* p_full = bars + 14;   // [2]
+  uint64_t* o_full = bars + 16;   // [2]
+  uint64_t* o_empty = bars + 18;  // [2]
+  uint64_t* mma_drain = bars + 20;  // teardown after a timed-out wait only
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 21);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 22);
+  volatile int* never_flag = reinterpret_cast<volatile int*>(bars + 23);  // never raised
+  int* armed = reinterpret_cast<int*>(bars + 24);  // [4]: phases armed on Q, K, V; the MMA thread had work
+  PgPlace* plan = reinterpret_cast<PgPlace*>(bars + 26);             // [2]
+  long long* warp_sum = reinterpret_cast<long long*>(bars + 32);     // [12]
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 8) {
+    if (lane == 0) {
+      mbar_init(q_full, 1);
+      mbar_init(q_empty, 1);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&k_full[i], 1);
+        mbar_init(&k_empty[i], 1);
+        mbar_init(&v_full[i], 1);
+        mbar_init(&v_empty[i], 1);
+        mbar_init(&v_ready[i], 1);
+        mbar_init(&s_full[i], 1);
+        mbar_init(&p_full[i], 128);
+        mbar_init(&o_full[i], 1);
+        mbar_init(&o_empty[i], 128);
+      }
+      mbar_init(mma_drain, 1);
+      *never_flag = 0;
+      armed[0] = armed[1] = armed[2] = armed[3] = 0;
+      // sampled once, so every thread of the CTA sees the same decision
+      *abort_flag = timed_out_before() ? 1 : 0;
+      fence_mbar_init();
+    }
+    __syncwarp();
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  const bool share = pg_plan<kTiles>(p, plan, warp_sum);  // has the barriers the set-up needs
+  tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
+  const uint32_t sbase = smem_u32(smem);
+  // after a recorded timeout elsewhere, do no work (but still free TMEM)
+  const bool work = share && !*abort_flag;
+  if (threadIdx.x == 0 && p.split) p.ws_desc[blockIdx.x] = PgDesc{};
+
+  if (warp >= 8) {
+    setmaxnreg_dec<104>();
+  }
+  if (warp == 8) {
+    // ------------------------------------------------------------ Q and K
+    if (work) {
+      PgWalk<kTiles> walk(p, plan);
+      PgItem it;
+      int n = 0, kt = 0;  // items and key tiles loaded
+      bool ok = true;
+      while (ok && walk.next(p, it)) {
+        if (n > 0 && !(ok = wait_bounded(q_empty, (n - 1) & 1, abort_flag))) break;
+        const bool has1 = kTiles == 2 && it.tokens > p.TQ;
+        if (lane == 0) {
+          const int bytes = p.TQ * p.G * 384;
+          mbar_arrive_expect_tx(q_full, has1 ? 2 * bytes : bytes);
+#pragma unroll
+          for (int c = 0; c < 3; ++c) tma_load_3d(smem + c * 16384, &tm_q, q_full, c * 64, it.g * p.G, it.tok0);
+          if (has1) {
+#pragma unroll
+            for (int c = 0; c < 3; ++c)
+              tma_load_3d(smem + kPgQBytes + c * 16384, &tm_q, q_full, c * 64, it.g * p.G, it.tok0 + p.TQ);
+          }
+        }
+        ++n;
+        for (int t = it.t0; t < it.t1; ++t, ++kt) {
+          const PgTile tl = pg_tile(it, t);
+          const int boxes = (tl.n + p.box_rows - 1) / p.box_rows;
+          const int row = lane < boxes ? pg_box_row(p, it, tl, lane) : 0;
+          const int ks = kt & 1;
+          if (kt >= 2 && !(ok = wait_bounded(&k_empty[ks], ((kt >> 1) - 1) & 1, abort_flag))) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&k_full[ks], boxes * p.box_rows * 384);
+            armed[1] = kt + 1;
+          }
+          __syncwarp();
+          if (lane < boxes) {
+            uint8_t* dst = smem + Lay::kOffK + ks * kPgKBytes + lane * p.box_rows * 128;
+#pragma unroll
+            for (int c = 0; c < 3; ++c) tma_load_3d(dst + c * 16384, &tm_k, &k_full[ks], c * 64, it.g, row);
+          }
+        }
+      }
+      if (lane == 0) armed[0] = n;  // every item counted had its Q armed
+    }
+  } else if (warp == 10) {
+    // ------------------------------------------------------------ V
+    if (work) {
+      PgWalk<kTiles> walk(p, plan);
+      PgItem it;
+      int kt = 0;
+      bool ok = true;
+      while (ok && walk.next(p, it)) {
+        for (int t = it.t0; t < it.t1; ++t, ++kt) {
+          const PgTile tl = pg_tile(it, t);
+          const int boxes = (tl.n + p.box_rows - 1) / p.box_rows;
+          const int row = lane < boxes ? pg_box_row(p, it, tl, lane) : 0;
+          const int vs = kt % kVStages;
+          if (kt >= kVStages && !(ok = wait_bounded(&v_empty[vs], (kt / kVStages - 1) & 1, abort_flag))) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&v_full[vs], boxes * p.box_rows * 256);
+            armed[2] = kt + 1;
+          }
+          __syncwarp();
+          if (lane < boxes) {
+            uint8_t* dst = smem + Lay::kOffV + vs * kPgVBytes + lane * p.box_rows * 128;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) tma_load_3d(dst + c * 16384, &tm_v, &v_full[vs], c * 64, it.g, row);
+          }
+        }
+      }
+    }
+  } else if (warp == 11) {
+    // ------------------------------------------------------------ value rows nothing sees
+    if (work) {
+      PgWalk<kTiles> walk(p, plan);
+      PgItem it;
+      int kt = 0;
+      bool ok = true;
+      while (ok && walk.next(p, it)) {
+        for (int t = it.t0; t < it.t1; ++t, ++kt) {
+          const PgTile tl = pg_tile(it, t);
+          const int vs = kt % kVStages;
+          // the stage is not refilled before this tile's P.V, which waits for v_ready
+          if (!(ok = wait_bounded(&v_full[vs], (kt / kVStages) & 1, abort_flag))) break;
+          uint8_t* vb = smem + Lay::kOffV + vs * kPgVBytes;
+          const int rows = tl.zlo + tl.n - tl.zhi;
+          for (int w = lane; w < rows * 16; w += 32) {  // 16 vectors a row: 8 in each 64-column box
+            const int i = w >> 4, r = i < tl.zlo ? i : tl.zhi + (i - tl.zlo);
+            *reinterpret_cast<uint4*>(vb + ((w >> 3) & 1) * 16384 + r * 128 + (w & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          if (rows > 0) fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&v_ready[vs]);
+        }
+      }
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0 && work) {
+      armed[3] = 1;
+      const uint32_t tS0 = tbase + 0, tS1 = tbase + 128, tO0 = tbase + 256, tO1 = tbase + 384;
+      constexpr uint32_t dhi = desc_hi_sw128(1024);
+      const uint32_t dQ0 = desc_lo_sw128(sbase, 16);
+      const uint32_t dQ1 = desc_lo_sw128(sbase + (kTiles - 1) * kPgQBytes, 16);
+      const uint32_t dK0 = desc_lo_sw128(sbase + Lay::kOffK, 16);
+      const uint32_t dV0 = desc_lo_sw128(sbase + Lay::kOffV, 16384);
+      constexpr uint32_t idesc_o = idesc_bf16_f32(128, 128, false, true);
+      // S = Q K^T over 192 dims = 12 MMAs of K=16 (3 swizzle boxes x 4 steps of 32 B), n keys wide
+      auto issue_s = [&](uint32_t tS, uint32_t dQ, int stage, int n) {
+        const uint32_t idesc = idesc_bf16_f32(128, 0, false, false) | (static_cast<uint32_t>(n >> 3) << 17);
+        const uint32_t dK = dK0 + static_cast<uint32_t>(stage) * (kPgKBytes >> 4);
+#pragma unroll
+        for (int kk = 0; kk < 12; ++kk) {
+          const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+          umma_ss_lo(tS, dQ + off, dK + off, dhi, idesc, kk > 0 ? 1u : 0u);
+        }
+      };
+      // O += P V over n keys (P: 8 TMEM columns for 16 keys; V: 16 rows = 2 KB)
+      auto issue_pv = [&](uint32_t tO, uint32_t tP, int stage, int n, bool acc) {
+        const uint32_t dV = dV0 + static_cast<uint32_t>(stage) * (kPgVBytes >> 4);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          if (kk * 16 < n) umma_ts_lo(tO, tP + kk * 8, dV + ((kk * 2048) >> 4), dhi, idesc_o, (acc || kk > 0) ? 1u : 0u);
+      };
+      PgWalk<kTiles> walk(p, plan);
+      PgItem it;
+      int n = 0, n1 = 0;   // items, those with a second tile
+      int kt = 0;          // key tiles (all items): K and V phases
+      int c0 = 0, c1 = 0;  // score tiles of tile 0 / 1: s_full, p_full phases (two tiles)
+      bool ok = true;
+      auto wait_v = [&]() { return wait_bounded(&v_ready[kt % kVStages], (kt / kVStages) & 1, abort_flag); };
+      while (ok && walk.next(p, it)) {
+        const bool has1 = kTiles == 2 && it.tokens > p.TQ;
+        if (!(ok = wait_bounded(q_full, n & 1, abort_flag))) break;
+        if constexpr (kTiles == 1) {
+          // scores run one key tile ahead of the softmax, in two TMEM buffers
+          auto scores = [&](int t, int kn) {
+            if (!wait_bounded(&k_full[kn & 1], (kn >> 1) & 1, abort_flag)) return false;
+            tc_fence_after();
+            issue_s((kn & 1) ? tS1 : tS0, dQ0, kn & 1, pg_tile(it, t).n);
+            umma_commit(&s_full[kn & 1]);
+            umma_commit(&k_empty[kn & 1]);
+            if (t == it.t1 - 1) umma_commit(q_empty);
+            return true;
+          };
+          if (!(ok = scores(it.t0, kt))) break;
+          if (it.t0 + 1 < it.t1 && !(ok = scores(it.t0 + 1, kt + 1))) break;
+          for (int t = it.t0; t < it.t1; ++t, ++kt) {
+            const PgTile tl = pg_tile(it, t);
+            if (!(ok = wait_v())) break;
+            if (!(ok = wait_bounded(&p_full[kt & 1], (kt >> 1) & 1, abort_flag))) break;
+            if (t == it.t0 && n > 0 && !(ok = wait_bounded(&o_empty[0], (n - 1) & 1, abort_flag))) break;
+            tc_fence_after();
+            issue_pv(tO0, (kt & 1) ? tS1 : tS0, kt % kVStages, tl.n, t > it.t0);
+            umma_commit(&v_empty[kt % kVStages]);
+            if (t == it.t1 - 1) umma_commit(&o_full[0]);
+            if (t + 2 < it.t1 && !(ok = scores(t + 2, kt + 2))) break;
+          }
+        } else {
+          if (!(ok = wait_bounded(&k_full[kt & 1], (kt >> 1) & 1, abort_flag))) break;
+          tc_fence_after();
+          {
+            const int w = pg_tile(it, it.t0).n;
+            issue_s(tS0, dQ0, kt & 1, w);
+            umma_commit(&s_full[0]);
+            if (has1) {
+              issue_s(tS1, dQ1, kt & 1, w);
+              umma_commit(&s_full[1]);
+            }
+            umma_commit(&k_empty[kt & 1]);
+            if (it.t1 - it.t0 == 1) umma_commit(q_empty);
+          }
+          for (int t = it.t0; t < it.t1; ++t, ++kt) {
+            const bool last = t == it.t1 - 1;
+            const PgTile tl = pg_tile(it, t);
+            const int wn = last ? 0 : pg_tile(it, t + 1).n;
+            if (!(ok = wait_v())) break;
+            if (!(ok = wait_bounded(&p_full[0], c0 & 1, abort_flag))) break;
+            // O_0 is free once the previous item's epilogue has read it
+            if (t == it.t0 && n > 0 && !(ok = wait_bounded(&o_empty[0], (n - 1) & 1, abort_flag))) break;
+            tc_fence_after();
+            issue_pv(tO0, tS0, 0, tl.n, t > it.t0);
+            ++c0;
+            if (last) umma_commit(&o_full[0]);
+            const int kn = kt + 1;
+            if (!last) {
+              if (!(ok = wait_bounded(&k_full[kn & 1], (kn >> 1) & 1, abort_flag))) break;
+              tc_fence_after();
+              issue_s(tS0, dQ0, kn & 1, wn);
+              umma_commit(&s_full[0]);
+              if (!has1 && t + 1 == it.t1 - 1) umma_commit(q_empty);
+            }
+            if (has1) {
+              if (!(ok = wait_bounded(&p_full[1], c1 & 1, abort_flag))) break;
+              if (t == it.t0 && n1 > 0 && !(ok = wait_bounded(&o_empty[1], (n1 - 1) & 1, abort_flag))) break;
+              tc_fence_after();
+              issue_pv(tO1, tS1, 0, tl.n, t > it.t0);
+              ++c1;
+              if (last) umma_commit(&o_full[1]);
+            }
+            umma_commit(&v_empty[0]);
+            if (!last) {
+              if (has1) {
+                issue_s(tS1, dQ1, kn & 1, wn);
+                umma_commit(&s_full[1]);
+                if (t + 1 == it.t1 - 1) umma_commit(q_empty);
+              }
+              umma_commit(&k_empty[kn & 1]);
+            }
+          }
+        }
+        ++n;
+        if (has1) ++n1;
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax / epilogue
+    setmaxnreg_inc<200>();
+    const int i = warp >> 2;          // which tile
+    const int r = threadIdx.x & 127;  // TMEM lane == row of the tile
+    const int tr = r / p.G, hr = r - tr * p.G;  // its token and head
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tO = tbase + lane_off + 256 + i * 128;
+    int n = 0;   // items this tile slot took part in
+    int tg = 0;  // score tiles it consumed
+    bool ok = true;
+    PgWalk<kTiles> walk(p, plan);
+    PgItem it;
+    while (ok && work && (kTiles == 2 || i == 0) && walk.next(p, it)) {
+      const int tokens = min(p.TQ, it.tokens - i * p.TQ);  // valid tokens of this tile
+      const bool whole = it.t0 == 0 && it.t1 == it.n_kt;
+      if (threadIdx.x == 0 && !whole) {
+        PgDesc* desc = p.ws_desc + blockIdx.x;
+        if (it.t0 > 0) {
+          desc->open0 = it.t1 == it.n_kt ? 2 : 1;
+        } else {
+          desc->open1 = 1;
+          desc->row0 = it.tok0;
+          desc->h0 = it.g * p.G;
+          desc->rows = it.tokens * p.G;
+        }
+      }
+      if (tokens <= 0) continue;  // no second tile
+      const bool row_ok = tr < tokens;
+      const bool warp_ok = __any_sync(0xffffffffu, row_ok);
+      const int pos0 = it.p0 + i * p.TQ, pos = pos0 + tr;
+      const int h = it.g * p.G + hr;
+      // the sink joins a whole item here, a divided one when its parts are joined
+      const bool sunk = whole && p.sinks && row_ok;
+      // a row of no token has a reference from the start, so that it never asks for one
+      float m = sunk ? p.sinks[h] * 1.4426950408889634f : row_ok ? -INFINITY : 0.f;
+      float l = sunk ? 1.f : 0.f;  // exact row sum (lse)
+      float lr = l;                // sum of the bf16-rounded P that enter P.V (output)
+      for (int t = it.t0; t < it.t1; ++t, ++tg) {
+        const int buf = kTiles == 1 ? (tg & 1) : i;
+        const int phase = kTiles == 1 ? (tg >> 1) & 1 : tg & 1;
+        const uint32_t tS = tbase + lane_off + buf * 128;
+        if (!(ok = wait_bounded(&s_full[buf], phase, abort_flag))) break;
+        tc_fence_after();
+        if (warp_ok) {
+          const int kpos0 = it.start + t * kPgKeys;
+          float s[128];
+          tmem_load128_sync(tS, s);
+          const bool full_tile = kpos0 + kPgKeys - 1 <= pos0 &&
+                                 (p.window == 0 || pos0 + tokens - 1 - kpos0 <= p.window - 1);
+          if (!full_tile) {
+            const int hi_k = pos - kpos0;                                      // keys <= hi_k visible
+            const int lo_k = p.window > 0 ? pos - p.window + 1 - kpos0 : -1;  // keys >= lo_k visible
+#pragma unroll
+            for (int c = 0; c < 128; ++c) s[c] = (c <= hi_k && c >= lo_k) ? s[c] : -INFINITY;
+          }
+          // Moves the reference m up to the row max of this tile where need is
+          // set (rescaling l, lr and, on later tiles, O by 2^(m_old - m_new)).
+          // The whole warp takes part: the O rescale is a warp-wide TMEM access.
+          auto move_max = [&](bool need) __attribute__((always_inline)) {
+            float mx8[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) mx8[k] = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 64; ++c) mx8[c & 7] = fmax3(mx8[c & 7], s[2 * c], s[2 * c + 1]);
+            const float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
+                                   fmaxf(mx8[6], mx8[7]));
+            const float m_new = fmaxf(m, mx * p.scale_log2);
+            float alpha = 1.f;
+            bool rescale_o = false;
+            if (need && m_new > m) {
+              alpha = ex2(m - m_new);  // 0 when m was -inf
+              l *= alpha;
+              lr *= alpha;
+              m = m_new;
+              rescale_o = t > it.t0;
+            }
+            if (__any_sync(0xffffffffu, rescale_o)) {
+              // O must hold the previous key tile's product: with two tiles S(t) was
+              // committed after it, with one it may still run
+              if (kTiles == 1) {
+                const int prev = tg - 1;
+                wait_bounded(&v_empty[prev % kVStages], (prev / kVStages) & 1, abort_flag);
+                tc_fence_after();
+              }
+#pragma unroll 1
+              for (int c = 0; c < 4; ++c) {
+                uint32_t o[32];
+                tmem_load32_sync(tO + c * 32, o);
+                const float a_ = rescale_o ? alpha : 1.f;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a_);
+                tmem_st32(tO + c * 32, o);
+              }
+            }
+          };
+          // P = 2^(s*scale - m), rounded to bf16 for the P.V product, written over
+          // the first 64 columns of S, and its two row sums.
+          float2 a, ar;
+          auto exps = [&]() __attribute__((always_inline)) {
+            const float neg_m = (m == -INFINITY) ? 0.f : -m;
+            const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
+            const float2 nm2 = make_float2(neg_m, neg_m);
+            float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            float2 acr[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              uint32_t pk[32];
+#pragma unroll
+              for (int c = 0; c < 32; ++c) {
+                const float2 x = fma2(make_float2(s[64 * half + 2 * c], s[64 * half + 2 * c + 1]), sc2, nm2);
+                const float2 e = make_float2(ex2(x.x), ex2(x.y));
+                pk[c] = pack_bf16(e.x, e.y);
+                acc[c & 1] = add2(acc[c & 1], e);
+                add_bf16x2(acr[c & 1], pk[c]);
+              }
+              tmem_st32(tS + 32 * half, pk);
+            }
+            a = add2(acc[0], acc[1]);
+            ar = add2(acr[0], acr[1]);
+          };
+          if (__any_sync(0xffffffffu, m == -INFINITY)) move_max(m == -INFINITY);
+          exps();
+          const auto unsafe = [&]() { return row_ok && !(a.x + a.y <= 0x1p64f); };  // also NaN
+          if (__any_sync(0xffffffffu, unsafe())) {
+            move_max(unsafe());
+            tmem_wait_st();  // the first P stores are complete before they are overwritten
+            exps();
+          }
+          l += a.x + a.y;
+          lr += ar.x + ar.y;
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        mbar_arrive(&p_full[buf]);
+      }
+      if (!ok) break;
+      // ---------------- epilogue: O is read out of TMEM first and released, so
+      // the next item's P.V can start at once.
+      if (!(ok = wait_bounded(&o_full[i], n & 1, abort_flag))) break;
+      tc_fence_after();
+      float o[128];
+      tmem_load128_sync(tO, o);
+      tc_fence_before();
+      mbar_arrive(&o_empty[i]);
+      ++n;
+      if (row_ok && !whole) {
+        const size_t slot = (size_t)blockIdx.x * 2 + (it.t0 == 0 ? 1 : 0);
+        const size_t row = slot * (kTiles * 128) + i * 128 + r;
+        if (MIMO_ROW_OK(row, (long long)gridDim.x * 2 * kTiles * 128)) {
+          p.ws_ml[row] = make_float4(m, l, lr, 0.f);
+          float* dst = p.ws_o + row * 128;
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            st_global_v8(dst + 8 * e, __float_as_uint(o[8 * e]), __float_as_uint(o[8 * e + 1]),
+                         __float_as_uint(o[8 * e + 2]), __float_as_uint(o[8 * e + 3]), __float_as_uint(o[8 * e + 4]),
+                         __float_as_uint(o[8 * e + 5]), __float_as_uint(o[8 * e + 6]), __float_as_uint(o[8 * e + 7]));
+        }
+      } else if (row_ok) {
+        const int tok = it.tok0 + i * p.TQ + tr;
+        if (MIMO_ROW_OK((long long)tok * p.Hq + h, (long long)p.pb.total_q * p.Hq)) {
+          const float f = (lr > 0.f) ? p.v_scale / lr : 0.f;
+          const size_t ob = ((size_t)tok * p.Hq + h) * 128;
+          if (p.out_f32) {
+            float* dst = reinterpret_cast<float*>(p.out) + ob;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              reinterpret_cast<float4*>(dst)[e] =
+                  make_float4(o[4 * e] * f, o[4 * e + 1] * f, o[4 * e + 2] * f, o[4 * e + 3] * f);
+          } else if (p.out_v8) {
+            __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.out) + ob;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              st_global_v8(dst + 16 * e, pack_bf16(o[16 * e + 0] * f, o[16 * e + 1] * f),
+                           pack_bf16(o[16 * e + 2] * f, o[16 * e + 3] * f),
+                           pack_bf16(o[16 * e + 4] * f, o[16 * e + 5] * f),
+                           pack_bf16(o[16 * e + 6] * f, o[16 * e + 7] * f),
+                           pack_bf16(o[16 * e + 8] * f, o[16 * e + 9] * f),
+                           pack_bf16(o[16 * e + 10] * f, o[16 * e + 11] * f),
+                           pack_bf16(o[16 * e + 12] * f, o[16 * e + 13] * f),
+                           pack_bf16(o[16 * e + 14] * f, o[16 * e + 15] * f));
+          } else {
+            uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.out) + ob);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              uint4 u;
+              u.x = pack_bf16(o[8 * e + 0] * f, o[8 * e + 1] * f);
+              u.y = pack_bf16(o[8 * e + 2] * f, o[8 * e + 3] * f);
+              u.z = pack_bf16(o[8 * e + 4] * f, o[8 * e + 5] * f);
+              u.w = pack_bf16(o[8 * e + 6] * f, o[8 * e + 7] * f);
+              dst[e] = u;
+            }
+          }
+          if (p.lse)
+            p.lse[(size_t)h * p.pb.total_q + tok] = (l > 0.f) ? (m * 0.6931471805599453f + logf(l)) : -INFINITY;
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag) {
+    // a role gave up: the loads and MMAs still in flight land before the CTA
+    // frees its TMEM and exits
+    if (warp == 8 && lane == 0) {
+      drain_armed(q_full, armed[0], never_flag);
+      drain_armed(&k_full[0], (armed[1] + 1) / 2, never_flag);
+      drain_armed(&k_full[1], armed[1] / 2, never_flag);
+      if (kVStages == 2) {
+        drain_armed(&v_full[0], (armed[2] + 1) / 2, never_flag);
+        drain_armed(&v_full[1], armed[2] / 2, never_flag);
+      } else {
+        drain_armed(v_full, armed[2], never_flag);
+      }
+    }
+    if (warp == 9 && lane == 0 && armed[3]) drain_mma(mma_drain, never_flag);  // MMAs may have been issued
+    __syncthreads();
+  }
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+// Joins the parts of each divided item and folds the sink in:
+//   M = max(sigma, max_c m_c),  Z = 2^(sigma-M) + sum_c 2^(m_c-M) l_c,
+//   out = v_scale * sum_c 2^(m_c-M) o_c / Z~,   lse = ln Z + M ln 2
+// where Z~ is Z over the parts' sums of the rounded P.  blockIdx.x: the CTA
+// whose share ends inside the item; its later parts are slot 0 of the CTAs
+// after it, up to the one where it ends.  One warp per row.
+template <int kTiles>
+__global__ void __launch_bounds__(256) paged_combine_kernel(const PagedAttnParams p) {
+  const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (timed_out_before()) return;  // after a recorded timeout: write nothing
+  const PgDesc d = p.ws_desc[c];
+  if (!d.open1) return;
+  int last = -1;  // the CTA where the item ends
+  for (int k0 = c + 1; k0 < (int)gridDim.x && last < 0; k0 += 32) {
+    const int k = k0 + lane;
+    const uint32_t ends = __ballot_sync(0xffffffffu, k < (int)gridDim.x && p.ws_desc[k].open0 == 2);
+    if (ends) last = k0 + __ffs(ends) - 1;
+  }
+  if (last < 0) return;  // a share gave up
+  constexpr int kRows = kTiles * 128;
+  const int per_tile = p.TQ * p.G;  // valid rows of a full tile
+  for (int v = blockIdx.y * 8 + warp; v < d.rows; v += gridDim.y * 8) {
+    const int tile = v / per_tile, r = tile * 128 + (v - tile * per_tile);
+    const int tok = d.row0 + v / p.G, h = d.h0 + v % p.G;
+    if (!MIMO_ROW_OK((long long)tok * p.Hq + h, (long long)p.pb.total_q * p.Hq)) continue;
+    const float sg = p.sinks ? p.sinks[h] * 1.4426950408889634f : -INFINITY;
+    float M = sg;
+    for (int k = c; k <= last; ++k)
+      M = fmaxf(M, p.ws_ml[((size_t)k * 2 + (k == c)) * kRows + r].x);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float Z = 0.f, Zr = 0.f;
+    if (M != -INFINITY) {
+      Z = (sg == -INFINITY) ? 0.f : ex2(sg - M);
+      Zr = Z;
+      for (int k = c; k <= last; ++k) {
+        const size_t row = ((size_t)k * 2 + (k == c)) * kRows + r;
+        const float4 ml = p.ws_ml[row];
+        const float w = (ml.x == -INFINITY) ? 0.f : ex2(ml.x - M);
+        Z += w * ml.y;
+        Zr += w * ml.z;
+        const float4 o = reinterpret_cast<const float4*>(p.ws_o + row * 128)[lane];
+        acc.x += w * o.x;
+        acc.y += w * o.y;
+        acc.z += w * o.z;
+        acc.w += w * o.w;
+      }
+    }
+    const float f = (Zr > 0.f) ? p.v_scale / Zr : 0.f;
+    const size_t ob = ((size_t)tok * p.Hq + h) * 32 + lane;
     if (p.out_f32)
-      reinterpret_cast<float4*>(p.out)[w * 32 + lane] = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+      reinterpret_cast<float4*>(p.out)[ob] = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
     else
-      reinterpret_cast<uint2*>(p.out)[w * 32 + lane] = make_uint2(pack_bf16(o.x * f, o.y * f), pack_bf16(o.z * f, o.w * f));
+      reinterpret_cast<uint2*>(p.out)[ob] = make_uint2(pack_bf16(acc.x * f, acc.y * f), pack_bf16(acc.z * f, acc.w * f));
     if (p.lse && lane == 0)
-      p.lse[(size_t)h * p.pb.total_q + t] = l > 0.f ? m * 0.6931471805599453f + logf(l) : -INFINITY;
+      p.lse[(size_t)h * p.pb.total_q + tok] = (Z > 0.f) ? (M * 0.6931471805599453f + logf(Z)) : -INFINITY;
   }
 }
 

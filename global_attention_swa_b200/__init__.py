@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
 
@@ -125,7 +126,7 @@ def _load():
     lib.mimo_attn_prefill_backward.argtypes = [dp, vp, vp, vp, vp, vp, vp, vp, i32, vp, i32, i32, i32,
                                                vp, vp, vp, vp, vp, sz, vp]
     lib.mimo_attn_prefill_backward.restype = i32
-    lib.mimo_attn_paged_attention_workspace_size.argtypes = [dp, i32, i32, i32]
+    lib.mimo_attn_paged_attention_workspace_size.argtypes = [dp, i32, i32, i32, i32]
     lib.mimo_attn_paged_attention_workspace_size.restype = sz
     lib.mimo_attn_paged_attention.argtypes = [dp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32,
                                               i32, vp, vp, vp, vp, sz, vp]
@@ -217,6 +218,8 @@ def _stream(stream, dev):
     """The stream to launch on: the caller's (which must belong to dev) or dev's
     current stream."""
     if stream is None:
+        if dev.index is not None:  # the handle alone, without a Stream object
+            return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(dev.index))
         stream = torch.cuda.current_stream(dev)
     elif stream.device != dev:
         raise ValueError(f"stream belongs to {stream.device}, but the call runs on {dev}")
@@ -438,22 +441,48 @@ def mimo_attn_prefill_backward(q, k, v, out, lse, dout, sinks, window, cu_seqlen
     return dq, dk, dv, ds
 
 
-def _paged_shapes(k_pages, v_pages, hkv, dqk, dv, block_table, cu_seqlens_q, seqlens):
-    """The pools and tables of a paged cache agree with each other."""
+_dims_ref = functools.lru_cache(maxsize=256)(lambda *args: ctypes.byref(make_dims(*args)))
+
+
+def _addr(t, name, dtype, shape, dev):
+    """Device address (0 for None) of a contiguous CUDA tensor of this dtype and shape on
+    dev: _shape, _same_device and _ptr in one look for the common case, and by their own
+    words where something is wrong."""
+    if t is None:
+        return 0
+    if t.shape != shape:
+        _shape(t, shape, name)
+    if t.device != dev:
+        _same_device(dev, **{name: t})
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
+        return _ptr(t, name, dtype).value
+    return t.data_ptr()
+
+
+def _call(fn, dev, *args):
+    """fn(*args, stream) with the tensors' device current; args[-1] is the caller's stream."""
+    args = (*args[:-1], _stream(args[-1], dev))
+    if dev.type != "cuda" or torch.cuda.current_device() == dev.index:
+        _check(fn(*args))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args))
+
+
+def _paged_pools(k_pages, v_pages, block_table):
+    """(num_pages, page_size, Hkv, Dqk, Dv, num_seqs, max_pages) of a paged cache."""
     if k_pages.dim() != 4 or v_pages.dim() != 4:
         raise ValueError("k_pages and v_pages must be [num_pages, page_size, Hkv, D]")
     if block_table.dim() != 2:
         raise ValueError("block_table must be [num_seqs, max_pages]")
-    _shape(k_pages, (k_pages.shape[0], k_pages.shape[1], hkv, dqk), "k_pages")
-    _shape(v_pages, (k_pages.shape[0], k_pages.shape[1], hkv, dv), "v_pages")
-    _shape(cu_seqlens_q, (block_table.shape[0] + 1,), "cu_seqlens_q")
-    _shape(seqlens, (block_table.shape[0],), "seqlens")
+    return (*k_pages.shape, v_pages.shape[3], *block_table.shape)
 
 
-def mimo_attn_paged_attention_workspace_size(hq, hkv, num_seqs, total_q, max_seqlen_q, dqk=192, dv=128):
+def mimo_attn_paged_attention_workspace_size(hq, hkv, num_seqs, total_q, max_seqlen_q, window=0, dqk=192,
+                                             dv=128):
     dims = make_dims(hq, hkv, dqk, dv)
     return int(lib.mimo_attn_paged_attention_workspace_size(ctypes.byref(dims), num_seqs, total_q,
-                                                            max_seqlen_q))
+                                                            max_seqlen_q, window))
 
 
 def mimo_attn_paged_attention(q, k_pages, v_pages, block_table, cu_seqlens_q, seqlens, max_seqlen_q,
@@ -468,33 +497,28 @@ def mimo_attn_paged_attention(q, k_pages, v_pages, block_table, cu_seqlens_q, se
     Returns (out [Nt,Hq,128], lse [Hq,Nt] fp32 or None).
     """
     nt, hq, dqk = q.shape
-    hkv, dv = k_pages.shape[-2], v_pages.shape[-1]
-    _paged_shapes(k_pages, v_pages, hkv, dqk, dv, block_table, cu_seqlens_q, seqlens)
-    _shape(sinks, (hq,), "sinks")
-    _shape(out, (nt, hq, dv), "out")
-    _shape(lse, (hq, nt), "lse")
+    P, ps, hkv, _, dv, B, M = _paged_pools(k_pages, v_pages, block_table)
     dev = q.device
+    addrs = (_addr(q, "q", _BF16, (nt, hq, dqk), dev), _addr(k_pages, "k_pages", _BF16, (P, ps, hkv, dqk), dev),
+             _addr(v_pages, "v_pages", _BF16, (P, ps, hkv, dv), dev),
+             _addr(block_table, "block_table", _I32, (B, M), dev),
+             _addr(cu_seqlens_q, "cu_seqlens_q", _I32, (B + 1,), dev), _addr(seqlens, "seqlens", _I32, (B,), dev))
+    sink = _addr(sinks, "sinks", _F32, (hq,), dev)
     if out is None:
         out = torch.empty((nt, hq, dv), dtype=out_dtype, device=dev)
     if lse is None and return_lse:
         lse = torch.empty((hq, nt), dtype=torch.float32, device=dev)
-    dims = make_dims(hq, hkv, dqk, dv, softmax_scale, v_scale, out.dtype)
-    B, M = block_table.shape
-    need = int(lib.mimo_attn_paged_attention_workspace_size(ctypes.byref(dims), B, nt, int(max_seqlen_q)))
+    max_seqlen_q, window = int(max_seqlen_q), int(window)
+    dims = _dims_ref(hq, hkv, dqk, dv, softmax_scale, v_scale, out.dtype)
+    need = lib.mimo_attn_paged_attention_workspace_size(dims, B, nt, max_seqlen_q, window)
     if need and workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _same_device(dev, k_pages=k_pages, v_pages=v_pages, block_table=block_table,
-                 cu_seqlens_q=cu_seqlens_q, seqlens=seqlens, sinks=sinks, out=out, lse=lse,
-                 workspace=workspace)
     wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    with _on_device(dev):
-        _check(lib.mimo_attn_paged_attention(
-            ctypes.byref(dims), _ptr(q, "q", _BF16), _ptr(k_pages, "k_pages", _BF16),
-            _ptr(v_pages, "v_pages", _BF16), _ptr(block_table, "block_table", _I32),
-            _ptr(cu_seqlens_q, "cu_seqlens_q", _I32), _ptr(seqlens, "seqlens", _I32), B, nt,
-            int(max_seqlen_q), k_pages.shape[0], k_pages.shape[1], M, int(window),
-            _ptr(sinks, "sinks", _F32), _ptr(out, "out", _OUT), _ptr(lse, "lse", _F32),
-            _ptr(workspace, "workspace"), wbytes, _stream(stream, dev)))
+    _call(lib.mimo_attn_paged_attention, dev, dims, *addrs, B, nt, max_seqlen_q, P, ps, M, window, sink,
+          _addr(out, "out", out.dtype if out.dtype in _OUT else _OUT, (nt, hq, dv), dev),
+          _addr(lse, "lse", _F32, (hq, nt), dev),
+          0 if workspace is None else _addr(workspace, "workspace", workspace.dtype, workspace.shape, dev),
+          wbytes, stream)
     return out, lse
 
 
@@ -503,35 +527,37 @@ def mimo_attn_paged_append(q, k_new, v_new, k_pages, v_pages, block_table, cu_se
     """Rotate the new tokens' q and k and write k, v into their pages (see
     include/mimo_attn.h).  Returns the rotated q: ``q_out`` (which may be q), or a new tensor."""
     nt, hq, dqk = q.shape
-    hkv, dv = k_pages.shape[-2], v_pages.shape[-1]
-    _paged_shapes(k_pages, v_pages, hkv, dqk, dv, block_table, cu_seqlens_q, seqlens)
-    _shape(k_new, (nt, hkv, dqk), "k_new")
-    _shape(v_new, (nt, hkv, dv), "v_new")
-    _shape(q_out, (nt, hq, dqk), "q_out")
+    P, ps, hkv, _, dv, B, M = _paged_pools(k_pages, v_pages, block_table)
     dev = q.device
     if q_out is None:
-        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    _same_device(dev, q_out=q_out, k_new=k_new, v_new=v_new, k_pages=k_pages, v_pages=v_pages,
-                 block_table=block_table, cu_seqlens_q=cu_seqlens_q, seqlens=seqlens)
-    dims = make_dims(hq, hkv, dqk, dv)
-    rd = dqk if rotary_dim is None else int(rotary_dim)
-    B, M = block_table.shape
-    with _on_device(dev):
-        _check(lib.mimo_attn_paged_append(
-            ctypes.byref(dims), _ptr(q, "q", _BF16), _ptr(q_out, "q_out", _BF16),
-            _ptr(k_new, "k_new", _BF16), _ptr(v_new, "v_new", _BF16),
-            _ptr(k_pages, "k_pages", _BF16), _ptr(v_pages, "v_pages", _BF16),
-            _ptr(block_table, "block_table", _I32), _ptr(cu_seqlens_q, "cu_seqlens_q", _I32),
-            _ptr(seqlens, "seqlens", _I32), B, nt, k_pages.shape[0], k_pages.shape[1], M,
-            float(rope_theta), rd, _stream(stream, dev)))
+        q_out = torch.empty((nt, hq, dqk), dtype=_BF16, device=dev)
+    _call(lib.mimo_attn_paged_append, dev, _dims_ref(hq, hkv, dqk, dv),
+          _addr(q, "q", _BF16, (nt, hq, dqk), dev), _addr(q_out, "q_out", _BF16, (nt, hq, dqk), dev),
+          _addr(k_new, "k_new", _BF16, (nt, hkv, dqk), dev), _addr(v_new, "v_new", _BF16, (nt, hkv, dv), dev),
+          _addr(k_pages, "k_pages", _BF16, (P, ps, hkv, dqk), dev),
+          _addr(v_pages, "v_pages", _BF16, (P, ps, hkv, dv), dev),
+          _addr(block_table, "block_table", _I32, (B, M), dev),
+          _addr(cu_seqlens_q, "cu_seqlens_q", _I32, (B + 1,), dev), _addr(seqlens, "seqlens", _I32, (B,), dev),
+          B, nt, P, ps, M, float(rope_theta), dqk if rotary_dim is None else int(rotary_dim), stream)
     return q_out
 
 
-def _page_table_shapes(page_refs, block_table, refs_out, table_out, rows_out):
+def _page_table(page_refs, block_table):
     if page_refs.dim() != 1 or block_table.dim() != 2:
         raise ValueError("page_refs must be [num_pages] and block_table [num_seqs, max_pages]")
-    _shape(refs_out, page_refs.shape, "refs_out")
-    _shape(table_out, (rows_out, block_table.shape[1]), "table_out")
+    return (page_refs.shape[0], *block_table.shape)
+
+
+def _ints(shape, dev):
+    return torch.empty(shape, dtype=_I32, device=dev)
+
+
+def _page_workspace(workspace, need, dev):
+    """(tensor, address, bytes) of the caller's workspace, or of a new one."""
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    return (workspace, _addr(workspace, "workspace", workspace.dtype, workspace.shape, dev),
+            workspace.numel() * workspace.element_size())
 
 
 def mimo_attn_page_hold(page_refs, block_table, seqlens, page_size, first=None, write_from=None,
@@ -544,35 +570,19 @@ def mimo_attn_page_hold(page_refs, block_table, seqlens, page_size, first=None, 
     Returns (refs_out, table_out, moves [B,2] for mimo_attn_page_copy, info [2]: pages
     missing (nothing was changed if > 0), pages free afterwards).
     """
-    B, M = block_table.shape
-    _page_table_shapes(page_refs, block_table, refs_out, table_out, B)
-    for name, t in (("seqlens", seqlens), ("first", first), ("write_from", write_from)):
-        _shape(t, (B,), name)
-    _shape(moves, (B, 2), "moves")
-    _shape(info, (2,), "info")
+    P, B, M = _page_table(page_refs, block_table)
     dev = page_refs.device
-    if refs_out is None:
-        refs_out = torch.empty_like(page_refs)
-    if table_out is None:
-        table_out = torch.empty_like(block_table, memory_format=torch.contiguous_format)
-    if moves is None:
-        moves = torch.empty((B, 2), dtype=torch.int32, device=dev)
-    if info is None:
-        info = torch.empty(2, dtype=torch.int32, device=dev)
-    need = int(lib.mimo_attn_page_hold_workspace_size(page_refs.numel()))
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _same_device(dev, block_table=block_table, seqlens=seqlens, first=first, write_from=write_from,
-                 refs_out=refs_out, table_out=table_out, moves=moves, info=info, workspace=workspace)
-    with _on_device(dev):
-        _check(lib.mimo_attn_page_hold(
-            _ptr(page_refs, "page_refs", _I32), page_refs.numel(),
-            _ptr(block_table, "block_table", _I32), B, M, int(page_size),
-            _ptr(seqlens, "seqlens", _I32), _ptr(first, "first", _I32),
-            _ptr(write_from, "write_from", _I32), _ptr(refs_out, "refs_out", _I32),
-            _ptr(table_out, "table_out", _I32), _ptr(moves, "moves", _I32), _ptr(info, "info", _I32),
-            _ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(),
-            _stream(stream, dev)))
+    refs_out = _ints((P,), dev) if refs_out is None else refs_out
+    table_out = _ints((B, M), dev) if table_out is None else table_out
+    moves = _ints((B, 2), dev) if moves is None else moves
+    info = _ints((2,), dev) if info is None else info
+    ws, ws_addr, ws_bytes = _page_workspace(workspace, lib.mimo_attn_page_hold_workspace_size(P), dev)
+    _call(lib.mimo_attn_page_hold, dev, _addr(page_refs, "page_refs", _I32, (P,), dev), P,
+          _addr(block_table, "block_table", _I32, (B, M), dev), B, M, int(page_size),
+          _addr(seqlens, "seqlens", _I32, (B,), dev), _addr(first, "first", _I32, (B,), dev),
+          _addr(write_from, "write_from", _I32, (B,), dev), _addr(refs_out, "refs_out", _I32, (P,), dev),
+          _addr(table_out, "table_out", _I32, (B, M), dev), _addr(moves, "moves", _I32, (B, 2), dev),
+          _addr(info, "info", _I32, (2,), dev), ws_addr, ws_bytes, stream)
     return refs_out, table_out, moves, info
 
 
@@ -582,21 +592,14 @@ def mimo_attn_page_fork(page_refs, block_table, parent, refs_out=None, table_out
     be block_table.  Returns (refs_out, table_out)."""
     if parent.dim() != 1:
         raise ValueError("parent must be 1-D")
-    B, M = block_table.shape
-    n = parent.numel()
-    _page_table_shapes(page_refs, block_table, refs_out, table_out, n)
+    P, B, M = _page_table(page_refs, block_table)
+    n = parent.shape[0]
     dev = page_refs.device
-    if refs_out is None:
-        refs_out = torch.empty_like(page_refs)
-    if table_out is None:
-        table_out = torch.empty((n, M), dtype=torch.int32, device=dev)
-    _same_device(dev, block_table=block_table, parent=parent, refs_out=refs_out, table_out=table_out)
-    with _on_device(dev):
-        _check(lib.mimo_attn_page_fork(
-            _ptr(page_refs, "page_refs", _I32), page_refs.numel(),
-            _ptr(block_table, "block_table", _I32), B, M, _ptr(parent, "parent", _I32), n,
-            _ptr(refs_out, "refs_out", _I32), _ptr(table_out, "table_out", _I32),
-            _stream(stream, dev)))
+    refs_out = _ints((P,), dev) if refs_out is None else refs_out
+    table_out = _ints((n, M), dev) if table_out is None else table_out
+    _call(lib.mimo_attn_page_fork, dev, _addr(page_refs, "page_refs", _I32, (P,), dev), P,
+          _addr(block_table, "block_table", _I32, (B, M), dev), B, M, _addr(parent, "parent", _I32, (n,), dev), n,
+          _addr(refs_out, "refs_out", _I32, (P,), dev), _addr(table_out, "table_out", _I32, (n, M), dev), stream)
     return refs_out, table_out
 
 
@@ -608,32 +611,19 @@ def mimo_attn_page_compact(page_refs, block_table, max_moves, refs_out=None, tab
     Returns (refs_out, table_out, moves [max_moves,2] for mimo_attn_page_copy, info [2]:
     moves made, pages in use).
     """
-    B, M = block_table.shape
-    _page_table_shapes(page_refs, block_table, refs_out, table_out, B)
+    P, B, M = _page_table(page_refs, block_table)
     max_moves = int(max_moves)
-    _shape(moves, (max_moves, 2), "moves")
-    _shape(info, (2,), "info")
     dev = page_refs.device
-    if refs_out is None:
-        refs_out = torch.empty_like(page_refs)
-    if table_out is None:
-        table_out = torch.empty_like(block_table, memory_format=torch.contiguous_format)
-    if moves is None:
-        moves = torch.empty((max_moves, 2), dtype=torch.int32, device=dev)
-    if info is None:
-        info = torch.empty(2, dtype=torch.int32, device=dev)
-    need = int(lib.mimo_attn_page_compact_workspace_size(page_refs.numel()))
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _same_device(dev, block_table=block_table, refs_out=refs_out, table_out=table_out, moves=moves,
-                 info=info, workspace=workspace)
-    with _on_device(dev):
-        _check(lib.mimo_attn_page_compact(
-            _ptr(page_refs, "page_refs", _I32), page_refs.numel(),
-            _ptr(block_table, "block_table", _I32), B, M, max_moves,
-            _ptr(refs_out, "refs_out", _I32), _ptr(table_out, "table_out", _I32),
-            _ptr(moves, "moves", _I32), _ptr(info, "info", _I32), _ptr(workspace, "workspace"),
-            workspace.numel() * workspace.element_size(), _stream(stream, dev)))
+    refs_out = _ints((P,), dev) if refs_out is None else refs_out
+    table_out = _ints((B, M), dev) if table_out is None else table_out
+    moves = _ints((max_moves, 2), dev) if moves is None else moves
+    info = _ints((2,), dev) if info is None else info
+    ws, ws_addr, ws_bytes = _page_workspace(workspace, lib.mimo_attn_page_compact_workspace_size(P), dev)
+    _call(lib.mimo_attn_page_compact, dev, _addr(page_refs, "page_refs", _I32, (P,), dev), P,
+          _addr(block_table, "block_table", _I32, (B, M), dev), B, M, max_moves,
+          _addr(refs_out, "refs_out", _I32, (P,), dev), _addr(table_out, "table_out", _I32, (B, M), dev),
+          _addr(moves, "moves", _I32, (max_moves, 2), dev), _addr(info, "info", _I32, (2,), dev), ws_addr,
+          ws_bytes, stream)
     return refs_out, table_out, moves, info
 
 
@@ -643,17 +633,12 @@ def mimo_attn_page_copy(k_pages, v_pages, moves, stream=None):
     [layers,P,...] of several.  Returns (k_pages, v_pages)."""
     if k_pages.dim() not in (4, 5) or k_pages.dim() != v_pages.dim():
         raise ValueError("k_pages and v_pages must be [num_pages, page_size, Hkv, D], or with a layer axis first")
-    _shape(v_pages, (*k_pages.shape[:-1], v_pages.shape[-1]), "v_pages")
-    _shape(moves, (moves.shape[0], 2), "moves")
-    P, ps, hkv, dqk = k_pages.shape[-4:]
-    dev = k_pages.device
-    _same_device(dev, v_pages=v_pages, moves=moves)
-    dims = make_dims(hkv, hkv, dqk, v_pages.shape[-1])
-    with _on_device(dev):
-        _check(lib.mimo_attn_page_copy(
-            ctypes.byref(dims), _ptr(k_pages, "k_pages", _BF16), _ptr(v_pages, "v_pages", _BF16),
-            k_pages.shape[0] if k_pages.dim() == 5 else 1, P, ps, _ptr(moves, "moves", _I32),
-            moves.shape[0], _stream(stream, dev)))
+    shape = k_pages.shape
+    P, ps, hkv, dqk = shape[-4:]
+    dv, n, dev = v_pages.shape[-1], moves.shape[0], k_pages.device
+    _call(lib.mimo_attn_page_copy, dev, _dims_ref(hkv, hkv, dqk, dv), _addr(k_pages, "k_pages", _BF16, shape, dev),
+          _addr(v_pages, "v_pages", _BF16, (*shape[:-1], dv), dev), shape[0] if len(shape) == 5 else 1, P, ps,
+          _addr(moves, "moves", _I32, (n, 2), dev), n, stream)
     return k_pages, v_pages
 
 

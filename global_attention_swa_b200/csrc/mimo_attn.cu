@@ -941,6 +941,16 @@ bool paged_one_tile(const mimo_attn_dims_t* dims, int max_seqlen_q) {
   return max_seqlen_q <= 128 / (dims->num_heads_q / dims->num_heads_kv);
 }
 
+// Whether items are cut and their parts joined.  Under a short window an item
+// has at most four key tiles (boxes of 16 keys: the window, the block's other
+// tokens and at most 15 keys before them), and only whole items are dealt out:
+// joining parts would cost more than the shares' imbalance.
+constexpr int kPagedShortWindow = 512;
+bool paged_split(const mimo_attn_dims_t* dims, int tiles, int window) {
+  const long D = (long)tiles * (128 / (dims->num_heads_q / dims->num_heads_kv));
+  return !(window > 0 && window <= kPagedShortWindow && (window - 1L + D + 15 + 127) / 128 <= 4);
+}
+
 // Opt the paged attention into its dynamic shared memory once per device.
 mimo_status_t ensure_paged_attributes() {
   static std::atomic<bool> done[64];
@@ -960,13 +970,15 @@ mimo_status_t ensure_paged_attributes() {
   return MIMO_OK;
 }
 
-// The arrays of the page bookkeeping calls.
+// The arrays of the page bookkeeping calls.  Their kernels count in int32 a
+// stride past the last element.
+constexpr long kMaxTableEntries = 1L << 30;
 mimo_status_t check_page_table(const int32_t* page_refs, int num_pages, const int32_t* block_table,
                                int num_seqs, int max_pages, const int32_t* refs_out, const int32_t* table_out) {
   if (num_pages <= 0) return fail(MIMO_ERR_INVALID_ARG, "num_pages must be positive (got %d)", num_pages);
   if (num_seqs < 0 || max_pages < 0) return fail(MIMO_ERR_INVALID_ARG, "sizes must be non-negative");
-  if ((long)num_seqs * max_pages > 0x7fffffffL)
-    return fail(MIMO_ERR_UNSUPPORTED, "num_seqs * max_pages must fit in int32");
+  if ((long)num_seqs * max_pages > kMaxTableEntries || num_pages > kMaxTableEntries)
+    return fail(MIMO_ERR_UNSUPPORTED, "num_seqs * max_pages and num_pages must be at most 2^30");
   const bool entries = num_seqs > 0 && max_pages > 0;
   if (!page_refs || !refs_out || (entries && (!block_table || !table_out)))
     return fail(MIMO_ERR_INVALID_ARG, "page_refs, block_table and their outputs must be non-NULL");
@@ -1000,11 +1012,12 @@ mimo_status_t launch_cluster(void (*kernel)(Params), const Params& p, long eleme
 extern "C" {
 
 size_t mimo_attn_paged_attention_workspace_size(const mimo_attn_dims_t* dims, int num_seqs, int total_q,
-                                                int max_seqlen_q) {
-  if (!dims || dims->num_heads_q <= 0 || dims->num_heads_kv <= 0 || num_seqs <= 0 || total_q <= 0 ||
-      max_seqlen_q <= 0 || dims->num_heads_q / dims->num_heads_kv > 128)
+                                                int max_seqlen_q, int window) {
+  if (!dims || dims->num_heads_kv <= 0 || dims->num_heads_q < dims->num_heads_kv || num_seqs <= 0 ||
+      total_q <= 0 || max_seqlen_q <= 0 || dims->num_heads_q / dims->num_heads_kv > 128)
     return 0;
-  return paged_workspace(paged_one_tile(dims, max_seqlen_q) ? 1 : 2).bytes;
+  const int tiles = paged_one_tile(dims, max_seqlen_q) ? 1 : 2;
+  return paged_split(dims, tiles, window) ? paged_workspace(tiles).bytes : 0;
 }
 
 mimo_status_t mimo_attn_paged_attention(const mimo_attn_dims_t* dims, const void* q, const void* k_pages,
@@ -1030,7 +1043,8 @@ mimo_status_t mimo_attn_paged_attention(const mimo_attn_dims_t* dims, const void
     return fail(MIMO_ERR_INVALID_ARG, "q, k_pages, v_pages and out must be 16-byte aligned");
   const int tiles = paged_one_tile(dims, max_seqlen_q) ? 1 : 2;
   const PagedWorkspace ws = paged_workspace(tiles);
-  if (!workspace || workspace_bytes < ws.bytes || !aligned16(workspace))
+  const bool split = paged_split(dims, tiles, window);
+  if (split && (!workspace || workspace_bytes < ws.bytes || !aligned16(workspace)))
     return fail(MIMO_ERR_WORKSPACE, "workspace of %zu bytes, 16-byte aligned, is needed (got %zu)", ws.bytes,
                 workspace ? workspace_bytes : (size_t)0);
   if ((st = ensure_paged_attributes())) return st;
@@ -1054,12 +1068,10 @@ mimo_status_t mimo_attn_paged_attention(const mimo_attn_dims_t* dims, const void
   // 16, so that an item reads few keys more than it sees.
   int box = 128;
   while (page_size % box) box /= 2;
-  if (window > 0 && window <= 512) box = 16;
+  if (window > 0 && window <= kPagedShortWindow) box = 16;
   p.box_rows = box;
-  // With at most four key tiles to an item, only whole items are dealt out:
-  // joining parts would cost more than the shares' imbalance.
+  p.split = split;
   const int D = tiles * p.TQ;
-  p.split = !(window > 0 && (window - 1L + D + box - 1 + 127) / 128 <= 4);
   p.min_tiles = 2;
   p.scale_log2 = scale_log2_of(dims);
   p.v_scale = v_scale_of(dims);
@@ -1097,12 +1109,18 @@ mimo_status_t mimo_attn_paged_attention(const mimo_attn_dims_t* dims, const void
         tq, tk, tv, p);
   if ((st = cuda_check(cudaGetLastError(), "paged attention launch"))) return st;
   if (p.split) {
-    const dim3 grid(ctas, tiles == 1 ? 4 : 8);
-    if (tiles == 1)
-      mimo::paged_combine_kernel<1><<<grid, 256, 0, (cudaStream_t)stream>>>(p);
-    else
-      mimo::paged_combine_kernel<2><<<grid, 256, 0, (cudaStream_t)stream>>>(p);
-    if ((st = cuda_check(cudaGetLastError(), "paged combine launch"))) return st;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas, tiles == 1 ? 4 : 8);
+    cfg.blockDim = dim3(256);
+    cfg.stream = (cudaStream_t)stream;
+    cudaLaunchAttribute at[1];  // the launch's own latency overlaps the kernel before it
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if ((st = cuda_check(cudaLaunchKernelEx(&cfg, tiles == 1 ? mimo::paged_combine_kernel<1> : mimo::paged_combine_kernel<2>, p),
+                         "paged combine launch")))
+      return st;
   }
   return ok();
 }
@@ -1205,8 +1223,8 @@ mimo_status_t mimo_attn_page_fork(const int32_t* page_refs, int num_pages, const
   const int32_t* out = num_seqs_out > 0 ? block_table_out : block_table;
   mimo_status_t st = check_page_table(page_refs, num_pages, block_table, num_seqs, max_pages, page_refs_out, out);
   if (st) return st;
-  if ((long)num_seqs_out * max_pages > 0x7fffffffL)
-    return fail(MIMO_ERR_UNSUPPORTED, "num_seqs_out * max_pages must fit in int32");
+  if ((long)num_seqs_out * max_pages > kMaxTableEntries)
+    return fail(MIMO_ERR_UNSUPPORTED, "num_seqs_out * max_pages must be at most 2^30");
   if (num_seqs_out > 0 && max_pages > 0 && (!parent || !block_table_out || !aligned4(parent) || !aligned4(block_table_out)))
     return fail(MIMO_ERR_INVALID_ARG, "parent and block_table_out must be non-NULL and 4-byte aligned");
   if (num_seqs > 0 && num_seqs_out > 0 && max_pages > 0 &&

@@ -113,26 +113,51 @@ struct PageHoldParams {
   int P, B, M, page_size;
 };
 
-// What the call wants of one table entry.
-struct HoldEntry {
-  int b, j;
-  bool row_ok, wanted;
-  bool written;   // the page reaches past write_from: it must be this sequence's own
+// What the call wants of the entries of one row.
+struct HoldRow {
+  int lo, hi;      // entries [lo, hi) are wanted
+  int own;         // wanted entries from here on will be written
   int write_from;
+  bool ok;
 };
-__device__ __forceinline__ HoldEntry hold_entry(const PageHoldParams& p, int i) {
-  HoldEntry e;
-  e.b = i / p.M;
-  e.j = i - e.b * p.M;
-  const int len = p.seqlens[e.b];
-  const int first = p.first ? p.first[e.b] : 0;
-  e.write_from = p.write_from ? p.write_from[e.b] : len;
-  e.row_ok = len >= 0 && first >= 0 && e.write_from >= 0 && len <= (long long)p.M * p.page_size;
-  const int hi = (int)(((long long)len + p.page_size - 1) / p.page_size);
-  e.wanted = e.row_ok && e.j >= first / p.page_size && e.j < hi;
-  e.written = p.write_from && e.wanted && e.j >= e.write_from / p.page_size;
-  return e;
+__device__ __forceinline__ HoldRow hold_row(const PageHoldParams& p, int b) {
+  HoldRow r = {};
+  if (b >= p.B) return r;
+  const int len = p.seqlens[b];
+  const int first = p.first ? p.first[b] : 0;
+  r.write_from = p.write_from ? p.write_from[b] : len;
+  r.ok = len >= 0 && first >= 0 && r.write_from >= 0 && len <= (long long)p.M * p.page_size;
+  r.lo = first / p.page_size;
+  r.hi = (int)(((long long)len + p.page_size - 1) / p.page_size);
+  r.own = p.write_from ? r.write_from / p.page_size : r.hi;
+  return r;
 }
+
+// A lane's way through a run, 32 entries at a time: the entry's row and place,
+// and the row's wants, worked out again only where the row changes.
+struct HoldCursor {
+  int b, j;
+  HoldRow row;
+  __device__ __forceinline__ HoldCursor(const PageHoldParams& p, int i) {
+    b = i / p.M;
+    j = i - b * p.M;
+    row = hold_row(p, b);
+  }
+  __device__ __forceinline__ void step(const PageHoldParams& p) {
+    j += 32;
+    if (j >= p.M) {
+      do {
+        j -= p.M;
+        ++b;
+      } while (j >= p.M);
+      row = hold_row(p, b);
+    }
+  }
+  __device__ __forceinline__ bool wanted() const { return row.ok && j >= row.lo && j < row.hi; }
+  __device__ __forceinline__ bool written() const { return wanted() && j >= row.own; }
+};
+
+constexpr int kPtBatch = 4;  // loads in flight per lane
 
 // Passes, each ended by a cluster barrier: copy the counts; take the dropped
 // entries off them; count the free pages and the entries in need (fresh ones,
@@ -141,12 +166,13 @@ __device__ __forceinline__ HoldEntry hold_entry(const PageHoldParams& p, int i) 
 // pages when it is known whether the pages suffice, and those are put back if
 // they do not.  A written entry that is to be replaced is marked -2 - page in
 // table_out between the passes, since the counts that decided it then move.
+//
+// Bound by latency: five barriers and the passes between them.
 __global__ void __launch_bounds__(kPtThreads, 1) page_hold_kernel(const PageHoldParams p) {
   __shared__ PtShared sh;
   const int lane = threadIdx.x & 31;
   const int tid = blockIdx.x * kPtThreads + threadIdx.x, threads = gridDim.x * kPtThreads;
-  const int n = p.B * p.M;
-  const PtRun pages = pt_run(p.P), entries = pt_run(n);
+  const PtRun pages = pt_run(p.P), entries = pt_run(p.B * p.M);
 
   if (p.refs_out != p.refs)
     for (int i = tid; i < p.P; i += threads) p.refs_out[i] = p.refs[i];
@@ -154,43 +180,80 @@ __global__ void __launch_bounds__(kPtThreads, 1) page_hold_kernel(const PageHold
   if (tid == 0) p.ws[0] = 0;
   cluster_sync_all();
 
-  for (int i = entries.begin + lane; i < entries.end; i += 32) {
-    const HoldEntry e = hold_entry(p, i);
-    const int pg = p.table[i];
-    if (e.j == 0 && !e.row_ok) record_status(1 /* MIMO_ERR_INVALID_ARG */);
-    if (pg >= p.P) record_status(1 /* MIMO_ERR_INVALID_ARG */);
-    if (e.row_ok && !e.wanted && pg >= 0 && pg < p.P && atomicSub(&p.refs_out[pg], 1) <= 0)
-      record_status(1 /* MIMO_ERR_INVALID_ARG: a held page whose count says free */);
+  // entries that change at all in this warp's run: most warps have none
+  int need = 0;
+  bool touched = false;
+  if (entries.begin < entries.end) {
+    HoldCursor c(p, entries.begin + lane);
+    for (int i0 = entries.begin; i0 < entries.end; i0 += 32 * kPtBatch) {
+      int pg[kPtBatch];
+#pragma unroll
+      for (int u = 0; u < kPtBatch; ++u) {
+        const int i = i0 + 32 * u + lane;
+        pg[u] = i < entries.end ? p.table[i] : -1;
+      }
+#pragma unroll
+      for (int u = 0; u < kPtBatch; ++u) {
+        const int i = i0 + 32 * u + lane;
+        bool fresh = false;
+        if (i < entries.end) {
+          const bool has = pg[u] >= 0 && pg[u] < p.P, wanted = c.wanted();
+          if ((c.j == 0 && !c.row.ok) || pg[u] >= p.P) record_status(1 /* MIMO_ERR_INVALID_ARG */);
+          fresh = wanted && !has;
+          const bool drop = c.row.ok && !wanted && has;
+          if (drop && atomicSub(&p.refs_out[pg[u]], 1) <= 0)
+            record_status(1 /* MIMO_ERR_INVALID_ARG: a held page whose count says free */);
+          const int v = (has || !c.row.ok) ? pg[u] : -1;
+          if (p.table_out != p.table || v != pg[u]) p.table_out[i] = v;
+          touched |= fresh || drop;
+        }
+        need += __popc(__ballot_sync(0xffffffffu, fresh));
+        c.step(p);
+      }
+    }
   }
   cluster_sync_all();
 
-  int need = 0, free_pages = 0;
-  for (int i0 = entries.begin; i0 < entries.end; i0 += 32) {
-    const int i = i0 + lane;
-    bool take = false;
-    if (i < entries.end) {
-      const HoldEntry e = hold_entry(p, i);
-      const int pg = p.table[i];
-      const bool has = pg >= 0 && pg < p.P;
-      const bool split = e.written && has && __ldcg(&p.refs_out[pg]) > 1;
-      take = split || (e.wanted && !has);
-      p.table_out[i] = split ? -2 - pg : (has || !e.row_ok) ? pg : -1;
+  if (p.write_from && entries.begin < entries.end) {
+    need = 0;
+    HoldCursor c(p, entries.begin + lane);
+    for (int i0 = entries.begin; i0 < entries.end; i0 += 32) {
+      const int i = i0 + lane;
+      bool take = false;
+      if (i < entries.end && c.wanted()) {
+        const int v = p.table_out[i];
+        const bool split = c.written() && v >= 0 && __ldcg(&p.refs_out[v]) > 1;
+        take = split || v < 0;
+        if (split) p.table_out[i] = -2 - v;
+      }
+      touched |= take;
+      need += __popc(__ballot_sync(0xffffffffu, take));
+      c.step(p);
     }
-    need += __popc(__ballot_sync(0xffffffffu, take));
   }
-  for (int i0 = pages.begin; i0 < pages.end; i0 += 32) {
-    const int i = i0 + lane;
-    free_pages += __popc(__ballot_sync(0xffffffffu, i < pages.end && __ldcg(&p.refs_out[i]) == 0));
+  touched = __any_sync(0xffffffffu, touched);
+  int free_pages = 0;
+  for (int i0 = pages.begin; i0 < pages.end; i0 += 32 * kPtBatch) {
+    int v[kPtBatch];
+#pragma unroll
+    for (int u = 0; u < kPtBatch; ++u) {
+      const int i = i0 + 32 * u + lane;
+      v[u] = i < pages.end ? __ldcg(&p.refs_out[i]) : 1;
+    }
+#pragma unroll
+    for (int u = 0; u < kPtBatch; ++u) free_pages += __popc(__ballot_sync(0xffffffffu, v[u] == 0));
   }
   const PtOffsets off = pt_offsets(sh, need, free_pages);
   const int missing = max(0, off.total[0] - off.total[1]);
 
   if (missing > 0) {  // the same decision in every thread of the cluster
-    for (int i = entries.begin + lane; i < entries.end; i += 32) {
-      const HoldEntry e = hold_entry(p, i);
-      const int v = p.table_out[i];
-      if (e.row_ok && v <= -2) p.table_out[i] = -2 - v;
-      if (e.row_ok && !e.wanted && v >= 0 && atomicAdd(&p.refs_out[v], 1) == 0) atomicAdd(&p.ws[0], 1);
+    if (touched) {
+      HoldCursor c(p, entries.begin + lane);
+      for (int i = entries.begin + lane; i < entries.end; i += 32, c.step(p)) {
+        const int v = p.table_out[i];
+        if (c.row.ok && v <= -2) p.table_out[i] = -2 - v;
+        if (c.row.ok && !c.wanted() && v >= 0 && atomicAdd(&p.refs_out[v], 1) == 0) atomicAdd(&p.ws[0], 1);
+      }
     }
     cluster_sync_all();
     if (tid == 0) {
@@ -210,34 +273,32 @@ __global__ void __launch_bounds__(kPtThreads, 1) page_hold_kernel(const PageHold
   }
   cluster_sync_all();
 
-  rank = off.before[0];
-  for (int i0 = entries.begin; i0 < entries.end; i0 += 32) {
-    const int i = i0 + lane;
-    bool take = false, drop = false;
-    HoldEntry e = {};
-    int v = -1;
-    if (i < entries.end) {
-      e = hold_entry(p, i);
-      v = p.table_out[i];
-      take = e.row_ok && (v <= -2 || (e.wanted && v == -1));
-      drop = e.row_ok && !e.wanted && v >= 0;
-    }
-    const uint32_t f = __ballot_sync(0xffffffffu, take);
-    if (take) {
-      const int pg = __ldcg(&p.ws[1 + rank + __popc(f & ((1u << lane) - 1))]);
-      p.table_out[i] = pg;
-      p.refs_out[pg] = 1;
-      if (v <= -2) {
-        if (atomicSub(&p.refs_out[-2 - v], 1) == 1) atomicAdd(&p.ws[0], 1);
-        if ((long long)e.j * p.page_size < e.write_from) {  // at most one page of a sequence
-          p.moves[2 * e.b] = -2 - v;
-          p.moves[2 * e.b + 1] = pg;
+  if (touched) {
+    rank = off.before[0];
+    HoldCursor c(p, entries.begin + lane);
+    for (int i0 = entries.begin; i0 < entries.end; i0 += 32) {
+      const int i = i0 + lane;
+      const bool in = i < entries.end && c.row.ok;
+      const int v = in ? p.table_out[i] : 0;
+      const bool take = in && (v <= -2 || (v == -1 && c.wanted()));
+      const uint32_t f = __ballot_sync(0xffffffffu, take);
+      if (take) {
+        const int pg = __ldcg(&p.ws[1 + rank + __popc(f & ((1u << lane) - 1))]);
+        p.table_out[i] = pg;
+        p.refs_out[pg] = 1;
+        if (v <= -2) {
+          if (atomicSub(&p.refs_out[-2 - v], 1) == 1) atomicAdd(&p.ws[0], 1);
+          if ((long long)c.j * p.page_size < c.row.write_from) {  // at most one page of a sequence
+            p.moves[2 * c.b] = -2 - v;
+            p.moves[2 * c.b + 1] = pg;
+          }
         }
+      } else if (in && v >= 0 && !c.wanted()) {
+        p.table_out[i] = -1;
       }
-    } else if (drop) {
-      p.table_out[i] = -1;
+      rank += __popc(f);
+      c.step(p);
     }
-    rank += __popc(f);
   }
   cluster_sync_all();
   if (tid == 0) {
@@ -278,19 +339,31 @@ __global__ void __launch_bounds__(kPtThreads, 1) page_fork_kernel(const PageFork
       if (r >= 0 && r < rows) atomicAdd(&children[r], 1);
     }
     __syncthreads();
-    for (long long i = threadIdx.x; i < (long long)rows * p.M; i += kPtThreads) {
-      const int d = children[i / p.M] - 1;
-      const int pg = p.table[(long long)r0 * p.M + i];
+    const int step_b = kPtThreads / max(1, p.M), step_j = kPtThreads - step_b * p.M;
+    int b = p.M > 0 ? threadIdx.x / p.M : rows, j = threadIdx.x - b * p.M;
+    for (; b < rows; b += step_b, j += step_j) {
+      if (j >= p.M) {  // step_j < M: once at most
+        j -= p.M;
+        if (++b >= rows) break;
+      }
+      const int d = children[b] - 1;
+      const int pg = p.table[(long long)(r0 + b) * p.M + j];
       if (pg >= p.P) record_status(1 /* MIMO_ERR_INVALID_ARG */);
       if (d != 0 && pg >= 0 && pg < p.P && atomicAdd(&p.refs_out[pg], d) <= 0)
         record_status(1 /* MIMO_ERR_INVALID_ARG: a held page whose count says free */);
     }
     __syncthreads();
   }
-  for (int i = tid; i < p.B_out * p.M; i += threads) {
-    const int b = i / p.M, r = p.parent[b];
-    if (r >= p.B && i == b * p.M) record_status(1 /* MIMO_ERR_INVALID_ARG */);
-    p.table_out[i] = (r >= 0 && r < p.B) ? p.table[(long long)r * p.M + (i - b * p.M)] : -1;
+  const int step_b = threads / max(1, p.M), step_j = threads - step_b * p.M;
+  int b = p.M > 0 ? tid / p.M : p.B_out, j = tid - b * p.M;
+  for (; b < p.B_out; b += step_b, j += step_j) {
+    if (j >= p.M) {
+      j -= p.M;
+      if (++b >= p.B_out) break;
+    }
+    const int r = p.parent[b];
+    if (r >= p.B && j == 0) record_status(1 /* MIMO_ERR_INVALID_ARG */);
+    p.table_out[(long long)b * p.M + j] = (r >= 0 && r < p.B) ? p.table[(long long)r * p.M + j] : -1;
   }
 }
 

@@ -360,6 +360,8 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   // after a recorded timeout elsewhere, do no work (but still free TMEM)
   const bool work = share && !*abort_flag;
   if (threadIdx.x == 0 && p.split) p.ws_desc[blockIdx.x] = PgDesc{};
+  // the combine kernel may be set up while this one runs; it waits for its end
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (warp >= 8) {
     setmaxnreg_dec<104>();
@@ -811,6 +813,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
 template <int kTiles>
 __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedAttnParams p) {
   const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched before the parts are complete
   if (timed_out_before()) return;  // after a recorded timeout: write nothing
   const PgDesc d = p.ws_desc[c];
   if (!d.open1) return;

@@ -39,15 +39,24 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedBatch& p, int b) {
   return s;
 }
 
-// The sequence of packed row t: the last b with cu_q[b] <= t among those that
-// have rows (upper bound of t in cu_q, less one); -1 for a row that none owns.
+// The sequence of packed row t, found by the whole warp: how many sequences
+// end at or before t (32 of cu_q at a time, 32 runs of it first); -1 for a row
+// that none owns.  For a sound cu_q that is the sequence with cu_q[b] <= t <
+// cu_q[b+1]; for any other the caller's range check decides.
 __device__ __forceinline__ int paged_seq_of_row(const PagedBatch& p, int t) {
-  int lo = 0, hi = p.num_seqs;  // cu_q[lo] <= t < cu_q[hi] for a sound cu_q
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (p.cu_q[mid + 1] <= t) lo = mid + 1; else hi = mid;
+  const int lane = threadIdx.x & 31;
+  int b = 0, step = p.num_seqs;
+  while (step > 32) {  // sequences [b, b + step) are left
+    const int run = (step + 31) / 32;
+    const int at = b + min(step, (lane + 1) * run);
+    const int full = __popc(__ballot_sync(0xffffffffu, p.cu_q[at] <= t));
+    const int skip = min(step, full * run);
+    b += skip;
+    step = min(step - skip, run);
   }
-  return (lo < p.num_seqs && p.cu_q[lo] <= t) ? lo : -1;
+  const bool before = lane < step && p.cu_q[b + lane + 1] <= t;
+  b += __popc(__ballot_sync(0xffffffffu, before));
+  return (b < p.num_seqs && p.cu_q[b] <= t) ? b : -1;
 }
 
 // The page that holds positions [j * page_size, (j + 1) * page_size) of

@@ -347,10 +347,11 @@ mimo_status_t mimo_attn_decode_noalloc(const mimo_attn_dims_t* dims, const void*
  */
 
 /*
- * Bytes of device workspace mimo_attn_paged_attention needs for these sizes.
+ * Bytes of device workspace mimo_attn_paged_attention needs for these sizes
+ * (parts of items that are divided among SMs); 0 under a short window.
  */
 size_t mimo_attn_paged_attention_workspace_size(const mimo_attn_dims_t* dims, int num_seqs, int total_q,
-                                                int max_seqlen_q);
+                                                int max_seqlen_q, int window);
 
 /*
  * Attention of the new tokens over the paged cache, which already holds their
@@ -406,7 +407,8 @@ mimo_status_t mimo_attn_paged_append(const mimo_attn_dims_t* dims, const void* q
 
 /*
  * Page bookkeeping, wholly on the device (nothing is read back, so the calls can
- * be captured in a graph).  page_refs_out may be page_refs and, but for fork,
+ * be captured in a graph); num_pages and num_seqs * max_pages are at most 2^30
+ * (else MIMO_ERR_UNSUPPORTED).  page_refs_out may be page_refs and, but for fork,
  * block_table_out may be block_table (in place); otherwise the outputs must
  * not overlap the inputs.  Results are deterministic.  block_table entries at
  * or above num_pages are recorded as MIMO_ERR_INVALID_ARG and count as no page

@@ -42,6 +42,18 @@ def test_attention_refuses(bad, status):
     assert mimo.lib.mimo_attn_last_error().decode()
 
 
+def test_attention_workspace_contract():
+    need = mimo.mimo_attn_paged_attention_workspace_size(64, 4, 2, 8, 4)
+    assert need > 0
+    assert _attend(ws=0) == WORKSPACE and _attend(wsb=need - 1) == WORKSPACE and _attend(ws=FAKE + 8) == WORKSPACE
+    assert "workspace" in mimo.lib.mimo_attn_last_error().decode()
+    # more rows to a sequence: twice the rows to a part; a short window: no parts
+    assert mimo.mimo_attn_paged_attention_workspace_size(64, 4, 2, 80, 40) > need
+    assert mimo.mimo_attn_paged_attention_workspace_size(64, 4, 2, 80, 40, 129) == 0
+    assert mimo.mimo_attn_paged_attention_workspace_size(64, 4, 2, 80, 40, 4096) > 0
+    assert mimo.mimo_attn_paged_attention_workspace_size(64, 4, 0, 0, 0) == 0
+
+
 def test_attention_of_nothing_is_a_no_op():
     assert _attend(seqs=0) == OK
     assert _attend(total=0, most=0) == OK
@@ -157,7 +169,15 @@ def host(monkeypatch):
         return real(types.SimpleNamespace(is_cuda=True, is_contiguous=t.is_contiguous, dtype=t.dtype,
                                           data_ptr=t.data_ptr), name, dtype)
 
+    def host_addr(t, name, dtype, shape, dev):
+        if t is None:
+            return 0
+        mimo._shape(t, shape, name)
+        mimo._same_device(dev, **{name: t})
+        return host_ptr(t, name, dtype).value
+
     lib = _Recorder()
+    monkeypatch.setattr(mimo, "_addr", host_addr)
     monkeypatch.setattr(mimo, "lib", lib)
     monkeypatch.setattr(mimo, "_ptr", host_ptr)
     monkeypatch.setattr(mimo, "_stream", lambda stream, dev: None)

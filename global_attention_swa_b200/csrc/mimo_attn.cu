@@ -22,6 +22,7 @@
 #include "rope_append_kernel.cuh"
 #include "decode_merge_kernel.cuh"
 #include "paged_attention_kernel.cuh"
+#include "paged_window_kernel.cuh"
 #include "paged_append_kernel.cuh"
 #include "page_table_kernel.cuh"
 #include "page_copy_kernel.cuh"
@@ -951,6 +952,16 @@ bool paged_split(const mimo_attn_dims_t* dims, int tiles, int window) {
   return !(window > 0 && window <= kPagedShortWindow && (window - 1L + D + 15 + 127) / 128 <= 4);
 }
 
+// Blocks of 128 / G tokens whose keys under this window, boxes of 16 and the
+// block's other tokens included, fit one score tile of the window kernel: 2, 1
+// or 0 (the general kernel).
+int paged_window_blocks(const mimo_attn_dims_t* dims, int tiles, int window) {
+  const long TQ = 128 / (dims->num_heads_q / dims->num_heads_kv);
+  for (int blocks = tiles; blocks >= 1; --blocks)
+    if (window > 0 && window - 1L + blocks * TQ + mimo::kPwBoxRows - 1 <= mimo::kPwKeys) return blocks;
+  return 0;
+}
+
 // Opt the paged attention into its dynamic shared memory once per device.
 mimo_status_t ensure_paged_attributes() {
   static std::atomic<bool> done[64];
@@ -965,6 +976,14 @@ mimo_status_t ensure_paged_attributes() {
   if ((st = cuda_check(cudaFuncSetAttribute(mimo::paged_attention_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                             mimo::PgLayout<2>::kSmemBytes),
                        "paged attention smem attribute")))
+    return st;
+  if ((st = cuda_check(cudaFuncSetAttribute(mimo::paged_window_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            mimo::kPwSmemBytes),
+                       "paged window smem attribute")))
+    return st;
+  if ((st = cuda_check(cudaFuncSetAttribute(mimo::paged_window_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            mimo::kPwSmemBytes),
+                       "paged window smem attribute")))
     return st;
   done[dev].store(true, std::memory_order_release);
   return MIMO_OK;
@@ -1071,7 +1090,8 @@ mimo_status_t mimo_attn_paged_attention(const mimo_attn_dims_t* dims, const void
   if (window > 0 && window <= kPagedShortWindow) box = 16;
   p.box_rows = box;
   p.split = split;
-  const int D = tiles * p.TQ;
+  const int blocks = paged_window_blocks(dims, tiles, window);  // 0: the general kernel
+  const int D = (blocks ? blocks : tiles) * p.TQ;
   p.min_tiles = 2;
   p.scale_log2 = scale_log2_of(dims);
   p.v_scale = v_scale_of(dims);
@@ -1101,7 +1121,11 @@ mimo_status_t mimo_attn_paged_attention(const mimo_attn_dims_t* dims, const void
   // most total_q / D + num_seqs blocks
   const int ctas = p.split ? sm_count()
                            : (int)std::min<long>(sm_count(), ((long)total_q / D + num_seqs) * Hkv);
-  if (tiles == 1)
+  if (blocks == 1)
+    mimo::paged_window_kernel<1><<<ctas, mimo::kPwThreads, mimo::kPwSmemBytes, (cudaStream_t)stream>>>(tq, tk, tv, p);
+  else if (blocks == 2)
+    mimo::paged_window_kernel<2><<<ctas, mimo::kPwThreads, mimo::kPwSmemBytes, (cudaStream_t)stream>>>(tq, tk, tv, p);
+  else if (tiles == 1)
     mimo::paged_attention_kernel<1><<<ctas, mimo::kPgThreads, mimo::PgLayout<1>::kSmemBytes, (cudaStream_t)stream>>>(
         tq, tk, tv, p);
   else

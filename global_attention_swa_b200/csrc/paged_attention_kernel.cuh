@@ -228,10 +228,10 @@ __device__ __forceinline__ PgTile pg_tile(const PgItem& it, int t) {
 
 // This CTA's share.  All threads call it; plan (shared) holds the first place
 // and the one past the last afterwards.  Returns false where there is no share.
-template <int kTiles>
+template <int kTiles, int kThreads = kPgThreads>
 __device__ __forceinline__ bool pg_plan(const PagedAttnParams& p, PgPlace* plan, long long* warp_sum) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int each = (p.pb.num_seqs + kPgThreads - 1) / kPgThreads;
+  const int each = (p.pb.num_seqs + kThreads - 1) / kThreads;
   const int b0 = threadIdx.x * each, b1 = min(p.pb.num_seqs, b0 + each);
   long long mine = 0;
   for (int b = b0; b < b1; ++b) {
@@ -251,7 +251,7 @@ __device__ __forceinline__ bool pg_plan(const PagedAttnParams& p, PgPlace* plan,
   __syncthreads();
   long long before = 0, total = 0;
 #pragma unroll
-  for (int w = 0; w < kPgThreads / 32; ++w) {
+  for (int w = 0; w < kThreads / 32; ++w) {
     const long long x = warp_sum[w];
     if (w < warp) before += x;
     total += x;

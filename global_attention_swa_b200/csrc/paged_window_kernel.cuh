@@ -1,0 +1,465 @@
+// Attention of a chunk of new tokens over a paged cache under a window so
+// short that all keys of an item fit one score tile (tcgen05).
+//
+// A block is TQ = 128 / G consecutive new tokens of one sequence times the G
+// query heads of one key/value head: 128 rows that share their keys.  An item
+// is kBlocks blocks.  Together they see at most window - 1 + kBlocks * TQ
+// keys; loaded in boxes of 16 from the one that holds the first, that is at
+// most kPwKeys = 160 (window 129, 16 heads to a key/value head: 2 blocks of 8
+// tokens, 159).  So there is no online softmax: maximum, exponentials and sums
+// of a row are exact, and the work of an item is one Q K^T and one P V per
+// block.  What bounds such a layer is its queries and outputs, 40 KB a block
+// against 100 KB of keys and values from L2 for an item, so the roles run as
+// a pipeline over blocks: while one block's softmax runs, the next one's
+// scores are computed and the queries of the one after are on their way.
+//
+//   warp 12     loads: Q two buffers, a block ahead; K and V once per item,
+//               a lane per box of 16 keys (the page table is looked up here)
+//   warp 13     MMA issuer: S(n) = Q K^T into score buffer n & 1, then O = P(n-1) V
+//   warp 14     zeroes the value rows that nothing of the item sees
+//   warps 0-7   softmax: warpgroup s takes the blocks with n & 1 == s, one row
+//               per thread, two passes over its TMEM row
+//   warps 8-11  epilogue: O / l -> out, lse
+//
+// The value operand carries a third 64-column block of ones and P V runs 144
+// columns wide: columns 128..143 of O are the row sum of the bf16-rounded P,
+// which normalises the output (P is rounded because the tensor cores take
+// 16-bit operands beside bf16 V; the sums are fp32).
+//
+// TMEM: S_0 [0, 160), S_1 [160, 320), O [320, 448) + row sum [448, 464).
+#pragma once
+
+#include "paged_attention_kernel.cuh"
+
+#undef MIMO_FILE_ID
+#define MIMO_FILE_ID 15  // site numbers of the checked build
+
+namespace mimo {
+
+constexpr int kPwThreads = 480;
+constexpr int kPwKeys = 160;
+constexpr int kPwBoxRows = 16;
+constexpr int kPwKBox = kPwKeys * 128;                // [keys][64 dims], 1024-aligned
+constexpr int kPwOffQ = 0;                            // 2 buffers
+constexpr int kPwOffK = 2 * kPgQBytes;                // 3 boxes
+constexpr int kPwOffV = kPwOffK + 3 * kPwKBox;        // 2 boxes
+constexpr int kPwOffOnes = kPwOffV + 2 * kPwKBox;     // the third value block: ones
+constexpr int kPwOffML = kPwOffOnes + kPwKBox;        // [2][128] float4 (m, l, sink term, -)
+constexpr int kPwOffBar = kPwOffML + 2 * 128 * 16;
+constexpr int kPwSmemBytes = kPwOffBar + 512 + 1024;  // barriers, plan; alignment slack
+constexpr uint32_t kPwColO = 2 * kPwKeys, kPwColSum = kPwColO + 128;
+static_assert(kPwOffOnes % 1024 == 0 && kPwColSum + 16 <= 512 && kPwSmemBytes <= 227 * 1024, "window layout");
+
+// An item's keys: the first one loaded, how many (a multiple of 16), and the
+// rows [0, zlo) and [zhi, n) of them that nothing sees.
+__device__ __forceinline__ PgTile pw_keys(const PgItem& it) {
+  PgTile r;
+  r.k0 = it.start;
+  const int left = it.hi + 1 - it.start;
+  r.n = (left + 15) & ~15;
+  r.zlo = it.lo - it.start;
+  r.zhi = left;
+  return r;
+}
+
+template <int kBlocks>
+__global__ void __launch_bounds__(kPwThreads, 1)
+    paged_window_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_v, const PagedAttnParams p) {
+  extern __shared__ __align__(1024) uint8_t pwsmem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(pwsmem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kPwOffBar);
+  uint64_t* q_full = bars + 0;     // [2]
+  uint64_t* q_empty = bars + 2;    // [2]
+  uint64_t* k_full = bars + 4;
+  uint64_t* k_empty = bars + 5;
+  uint64_t* v_full = bars + 6;
+  uint64_t* v_empty = bars + 7;
+  uint64_t* v_ready = bars + 8;
+  uint64_t* s_full = bars + 10;    // [2]
+  uint64_t* p_full = bars + 12;    // [2]
+  uint64_t* o_full = bars + 14;
+  uint64_t* o_empty = bars + 15;
+  uint64_t* ml_full = bars + 16;   // [2]
+  uint64_t* ml_empty = bars + 18;  // [2]
+  uint64_t* mma_drain = bars + 20;  // teardown after a timed-out wait only
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 21);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 22);
+  volatile int* never_flag = reinterpret_cast<volatile int*>(bars + 23);  // never raised
+  PgPlace* plan = reinterpret_cast<PgPlace*>(bars + 24);          // [2]
+  long long* warp_sum = reinterpret_cast<long long*>(bars + 28);  // [15]
+  float4* ml = reinterpret_cast<float4*>(smem + kPwOffML);  // [2][128] (m, l, sink term) per row
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // phases armed: Q for blocks 0, 1, ... (buffer n & 1), K and V per item
+  int armed_q = 0, armed_k = 0, armed_v = 0;
+  for (int i = threadIdx.x; i < kPwKBox / 4; i += kPwThreads)
+    reinterpret_cast<uint32_t*>(smem + kPwOffOnes)[i] = 0x3F803F80u;  // bf16 1.0
+  fence_proxy_async_smem();
+  if (warp == 12) {
+    if (lane == 0) {
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&q_full[i], 1);
+        mbar_init(&q_empty[i], 1);
+        mbar_init(&s_full[i], 1);
+        mbar_init(&p_full[i], 128);
+        mbar_init(&ml_full[i], 128);
+        mbar_init(&ml_empty[i], 128);
+      }
+      mbar_init(k_full, 1);
+      mbar_init(k_empty, 1);
+      mbar_init(v_full, 1);
+      mbar_init(v_empty, 1);
+      mbar_init(v_ready, 1);
+      mbar_init(o_full, 1);
+      mbar_init(o_empty, 128);
+      mbar_init(mma_drain, 1);
+      *never_flag = 0;
+      *abort_flag = timed_out_before() ? 1 : 0;
+      fence_mbar_init();
+    }
+    __syncwarp();
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  const bool share = pg_plan<kBlocks, kPwThreads>(p, plan, warp_sum);  // has the barriers the set-up needs
+  tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
+  const uint32_t sbase = smem_u32(smem);
+  const bool work = share && !*abort_flag;
+
+  // Each role walks the same items, and the blocks of each: block n of the
+  // CTA's uses buffer n & 1.
+  PgWalk<kBlocks> walk(p, plan);
+  PgItem it;
+  const auto blocks_of = [&](const PgItem& x) { return kBlocks == 2 && x.tokens > p.TQ ? 2 : 1; };
+
+  if (!work) {
+    // no share, or a time-out elsewhere
+  } else if (warp == 12) {
+    // ------------------------------------------------------------ loads
+    const auto load_q = [&](const PgItem& x, int blk, int b) {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&q_full[b], p.TQ * p.G * 384);
+#pragma unroll
+        for (int c = 0; c < 3; ++c)
+          tma_load_3d(smem + kPwOffQ + b * kPgQBytes + c * 16384, &tm_q, &q_full[b], c * 64, x.g * p.G,
+                      x.tok0 + blk * p.TQ);
+      }
+      ++armed_q;
+    };
+    bool ok = true, have = walk.next(p, it);
+    int n = 0, kp = 0;
+    if (have) load_q(it, 0, 0);
+    PgTile keys = pw_keys(it);
+    int boxes = keys.n / kPwBoxRows;
+    int row = have && lane < boxes ? pg_box_row(p, it, keys, lane) : 0;
+    while (ok && have) {
+      const int nblk = blocks_of(it), bytes = boxes * kPwBoxRows * 128, row_now = row, boxes_now = boxes;
+      const int g = it.g;
+      for (int blk = 0; ok && blk < nblk; ++blk, ++n) {
+        if (blk == 0) {
+          if (kp >= 1 && !(ok = wait_bounded(k_empty, (kp - 1) & 1, abort_flag))) break;
+          if (lane == 0) mbar_arrive_expect_tx(k_full, 3 * bytes);
+          ++armed_k;
+          __syncwarp();
+          if (lane < boxes_now) {
+#pragma unroll
+            for (int c = 0; c < 3; ++c)
+              tma_load_3d(smem + kPwOffK + c * kPwKBox + lane * kPwBoxRows * 128, &tm_k, k_full, c * 64, g, row_now);
+          }
+          if (kp >= 1 && !(ok = wait_bounded(v_empty, (kp - 1) & 1, abort_flag))) break;
+          if (lane == 0) mbar_arrive_expect_tx(v_full, 2 * bytes);
+          ++armed_v;
+          __syncwarp();
+          if (lane < boxes_now) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              tma_load_3d(smem + kPwOffV + c * kPwKBox + lane * kPwBoxRows * 128, &tm_v, v_full, c * 64, g, row_now);
+          }
+          ++kp;
+        }
+        // the next block's Q, one block ahead (its buffer was freed by S(n-1));
+        // with the item's last block, the next item's pages too
+        const int bn = (n + 1) & 1;
+        const bool in_item = blk + 1 < nblk;
+        if (!in_item) {
+          have = walk.next(p, it);
+          if (!have) continue;
+          keys = pw_keys(it);
+          boxes = keys.n / kPwBoxRows;
+          row = lane < boxes ? pg_box_row(p, it, keys, lane) : 0;
+        }
+        if (n + 1 >= 2 && !(ok = wait_bounded(&q_empty[bn], (((n + 1) >> 1) - 1) & 1, abort_flag))) break;
+        load_q(it, in_item ? blk + 1 : 0, bn);
+      }
+    }
+  } else if (warp == 13) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t idesc_o = idesc_bf16_f32(128, 144, false, true);  // 128 value dims + 16 ones
+      const uint32_t tO = tbase + kPwColO;
+      bool ok = true;
+      // O = P(m) V over k keys: 16 to an MMA (P: 8 TMEM columns; V: 16 rows = 2 KB)
+      const auto do_pv = [&](int m, int item, int k, bool first_of_item, bool last_of_item) {
+        const int bm = m & 1;
+        if (!(ok = wait_bounded(&p_full[bm], (m >> 1) & 1, abort_flag))) return;
+        if (first_of_item && !(ok = wait_bounded(v_ready, item & 1, abort_flag))) return;
+        if (m >= 1 && !(ok = wait_bounded(o_empty, (m - 1) & 1, abort_flag))) return;
+        tc_fence_after();
+        const uint32_t tP = tbase + bm * kPwKeys;
+        const uint32_t aV = sbase + kPwOffV;
+        for (int kk = 0; kk < k / 16; ++kk)
+          umma_ts(tO, tP + kk * 8, smem_desc_sw128(aV + kk * 2048, kPwKBox, 1024), idesc_o, kk > 0 ? 1u : 0u);
+        if (last_of_item) umma_commit(v_empty);
+        umma_commit(o_full);
+      };
+      int n = 0, kp = 0;
+      int pm = -1, pkp = 0, pk = 0;  // previous block: number, item, keys
+      bool pfirst = false, plast = false;
+      while (ok && walk.next(p, it)) {
+        const int nblk = blocks_of(it), k = pw_keys(it).n;
+        const uint32_t idesc_s = idesc_bf16_f32(128, 0, false, false) | (static_cast<uint32_t>(k >> 3) << 17);
+        for (int blk = 0; ok && blk < nblk; ++blk, ++n) {
+          const int b = n & 1;
+          if (!(ok = wait_bounded(&q_full[b], (n >> 1) & 1, abort_flag))) break;
+          if (blk == 0 && !(ok = wait_bounded(k_full, kp & 1, abort_flag))) break;
+          tc_fence_after();
+          const uint32_t aQ = sbase + kPwOffQ + b * kPgQBytes;
+          const uint32_t aK = sbase + kPwOffK;
+          const uint32_t tS = tbase + b * kPwKeys;
+#pragma unroll
+          for (int kk = 0; kk < 12; ++kk) {
+            const uint32_t off = (kk & 3) * 32;
+            umma_ss(tS, smem_desc_sw128(aQ + (kk >> 2) * 16384 + off, 16, 1024),
+                    smem_desc_sw128(aK + (kk >> 2) * kPwKBox + off, 16, 1024), idesc_s, kk > 0 ? 1u : 0u);
+          }
+          umma_commit(&s_full[b]);
+          umma_commit(&q_empty[b]);
+          if (blk == nblk - 1) umma_commit(k_empty);
+          if (pm >= 0) do_pv(pm, pkp, pk, pfirst, plast);
+          pm = n;
+          pkp = kp;
+          pk = k;
+          pfirst = blk == 0;
+          plast = blk == nblk - 1;
+        }
+        ++kp;
+      }
+      if (ok && pm >= 0) do_pv(pm, pkp, pk, pfirst, plast);
+    }
+  } else if (warp == 14) {
+    // ------------------------------------------------------------ value rows nothing sees
+    int kp = 0;
+    while (walk.next(p, it)) {
+      const PgTile keys = pw_keys(it);
+      // not refilled before this item's P V, which waits for v_ready
+      if (!wait_bounded(v_full, kp & 1, abort_flag)) break;
+      const int rows = keys.zlo + keys.n - keys.zhi;
+      for (int w = lane; w < rows * 16; w += 32) {  // 16 vectors a row: 8 in each 64-column box
+        const int i = w >> 4, r = i < keys.zlo ? i : keys.zhi + (i - keys.zlo);
+        *reinterpret_cast<uint4*>(smem + kPwOffV + ((w >> 3) & 1) * kPwKBox + r * 128 + (w & 7) * 16) =
+            make_uint4(0, 0, 0, 0);
+      }
+      if (rows > 0) fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(v_ready);
+      ++kp;
+    }
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ softmax
+    const int s = warp >> 2;               // this warpgroup's blocks: n & 1 == s
+    const int r = (warp & 3) * 32 + lane;  // TMEM lane = row = token * G + head
+    const int a = r / p.G, hh = r - a * p.G;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    int n = 0;
+    bool ok = true;
+    while (ok && walk.next(p, it)) {
+      const int nblk = blocks_of(it);
+      const PgTile keys = pw_keys(it);
+      const int N = keys.n;
+      for (int blk = 0; ok && blk < nblk; ++blk, ++n) {
+        const int b = n & 1;
+        if (b != s) continue;
+        const int tokens = min(p.TQ, it.tokens - blk * p.TQ);
+        // rows 32 and up of this warp's quarter may hold no token at all
+        const bool warp_ok = __any_sync(0xffffffffu, a < tokens);
+        const int hg = it.g * p.G + hh;
+        const int qpos = it.p0 + blk * p.TQ + a;
+        const int c_hi = qpos - keys.k0;                              // keys <= qpos
+        const int c_lo = max(qpos - p.window + 1, 0) - keys.k0;       // keys in window, >= 0
+        const float sg2 = p.sinks && a < tokens ? p.sinks[hg] * 1.4426950408889634f : -INFINITY;
+        if (!(ok = wait_bounded(&s_full[b], (n >> 1) & 1, abort_flag))) break;
+        tc_fence_after();
+        const uint32_t tS = tbase + lane_off + b * kPwKeys;
+        float m = sg2;
+        float2 l2 = make_float2(0.f, 0.f);
+        if (warp_ok) {
+          // pass 1: row max over the visible columns, 48 at a time; columns at or
+          // past N lie outside [c_lo, c_hi] and are masked like the window's edges
+          float mx0 = -INFINITY, mx1 = -INFINITY;
+          for (int c0 = 0; c0 < N; c0 += 48) {
+            uint32_t v[48];
+            tmem_load48_sync(tS + c0, v);
+#pragma unroll
+            for (int q = 0; q < 3; ++q) {
+              const int cq0 = c0 + 16 * q;
+              if (cq0 >= c_lo && cq0 + 15 <= c_hi) {
+#pragma unroll
+                for (int e = 0; e < 16; e += 4) {
+                  mx0 = fmax3(mx0, __uint_as_float(v[16 * q + e]), __uint_as_float(v[16 * q + e + 1]));
+                  mx1 = fmax3(mx1, __uint_as_float(v[16 * q + e + 2]), __uint_as_float(v[16 * q + e + 3]));
+                }
+              } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  const int c = cq0 + e;
+                  if (c >= c_lo && c <= c_hi) mx0 = fmaxf(mx0, __uint_as_float(v[16 * q + e]));
+                }
+              }
+            }
+          }
+          m = fmaxf(sg2, fmaxf(mx0, mx1) * p.scale_log2);
+          const float neg_m = (m == -INFINITY) ? 0.f : -m;
+          // pass 2: P = 2^(s*scale - m) (0 outside the window), bf16 over the same
+          // columns (P of columns [c0, c0 + 48) lands in [c0 / 2, c0 / 2 + 24), behind
+          // the read position); the unrounded sum gives lse
+          for (int c0 = 0; c0 < N; c0 += 48) {
+            uint32_t v[48];
+            tmem_load48_sync(tS + c0, v);
+#pragma unroll
+            for (int q = 0; q < 3; ++q) {
+              const int cq0 = c0 + 16 * q;
+              uint32_t pk[8];
+              if (cq0 >= c_lo && cq0 + 15 <= c_hi) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const float2 x =
+                      fma2(make_float2(__uint_as_float(v[16 * q + 2 * e]), __uint_as_float(v[16 * q + 2 * e + 1])),
+                           make_float2(p.scale_log2, p.scale_log2), make_float2(neg_m, neg_m));
+                  const float2 pe = make_float2(ex2(x.x), ex2(x.y));
+                  pk[e] = pack_bf16(pe.x, pe.y);
+                  l2 = add2(l2, pe);
+                }
+              } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const int c = cq0 + 2 * e;
+                  const float x0 = fmaf(__uint_as_float(v[16 * q + 2 * e]), p.scale_log2, neg_m);
+                  const float x1 = fmaf(__uint_as_float(v[16 * q + 2 * e + 1]), p.scale_log2, neg_m);
+                  const float2 pe = make_float2((c >= c_lo && c <= c_hi) ? ex2(x0) : 0.f,
+                                                (c + 1 >= c_lo && c + 1 <= c_hi) ? ex2(x1) : 0.f);
+                  pk[e] = pack_bf16(pe.x, pe.y);
+                  l2 = add2(l2, pe);
+                }
+              }
+              if (cq0 < N) tmem_st8(tS + cq0 / 2, pk);
+            }
+          }
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        mbar_arrive(&p_full[b]);
+        const float ps = (sg2 != -INFINITY) ? ex2(sg2 - m) : 0.f;  // the sink's term
+        if (n >= 2 && !(ok = wait_bounded(&ml_empty[b], ((n >> 1) - 1) & 1, abort_flag))) break;
+        ml[b * 128 + r] = make_float4(m, l2.x + l2.y + ps, ps, 0.f);
+        mbar_arrive(&ml_full[b]);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int r = threadIdx.x - 256;
+    const int a = r / p.G, hh = r - a * p.G;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tO = tbase + lane_off + kPwColO;
+    int n = 0;
+    bool ok = true;
+    while (ok && walk.next(p, it)) {
+      const int nblk = blocks_of(it);
+      for (int blk = 0; ok && blk < nblk; ++blk, ++n) {
+        const int b = n & 1;
+        if (!(ok = wait_bounded(o_full, n & 1, abort_flag))) break;
+        tc_fence_after();
+        if (!(ok = wait_bounded(&ml_full[b], (n >> 1) & 1, abort_flag))) break;
+        const float4 mlv = ml[b * 128 + r];  // m (base 2), unrounded sum with the sink, the sink's term
+        mbar_arrive(&ml_empty[b]);
+        float rs[16];
+        tmem_load16_sync(tbase + lane_off + kPwColSum, rs);  // rounded-P row sum (16 equal columns)
+        const float lr = rs[0] + mlv.z;
+        const int tok = it.tok0 + blk * p.TQ + a;
+        const int hg = it.g * p.G + hh;
+        const bool live = a < min(p.TQ, it.tokens - blk * p.TQ) &&
+                          MIMO_ROW_OK((long long)tok * p.Hq + hg, (long long)p.pb.total_q * p.Hq);
+        const float f = (lr > 0.f) ? p.v_scale / lr : 0.f;
+        const size_t ob = ((size_t)tok * p.Hq + hg) * 128;
+        // O in two 64-column halves (480 threads leave 136 registers each); it is
+        // released to the next P V after the second half is in registers
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          float o[64];
+          tmem_load64_sync(tO + h * 64, o);
+          if (h == 1) {
+            tc_fence_before();
+            mbar_arrive(o_empty);
+          }
+          if (!live) continue;
+          if (p.out_f32) {
+            float* dst = reinterpret_cast<float*>(p.out) + ob + h * 64;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              reinterpret_cast<float4*>(dst)[e] =
+                  make_float4(o[4 * e] * f, o[4 * e + 1] * f, o[4 * e + 2] * f, o[4 * e + 3] * f);
+          } else if (p.out_v8) {
+            __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.out) + ob + h * 64;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              st_global_v8(dst + 16 * e, pack_bf16(o[16 * e + 0] * f, o[16 * e + 1] * f),
+                           pack_bf16(o[16 * e + 2] * f, o[16 * e + 3] * f),
+                           pack_bf16(o[16 * e + 4] * f, o[16 * e + 5] * f),
+                           pack_bf16(o[16 * e + 6] * f, o[16 * e + 7] * f),
+                           pack_bf16(o[16 * e + 8] * f, o[16 * e + 9] * f),
+                           pack_bf16(o[16 * e + 10] * f, o[16 * e + 11] * f),
+                           pack_bf16(o[16 * e + 12] * f, o[16 * e + 13] * f),
+                           pack_bf16(o[16 * e + 14] * f, o[16 * e + 15] * f));
+          } else {
+            uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.out) + ob + h * 64);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              uint4 u;
+              u.x = pack_bf16(o[8 * e + 0] * f, o[8 * e + 1] * f);
+              u.y = pack_bf16(o[8 * e + 2] * f, o[8 * e + 3] * f);
+              u.z = pack_bf16(o[8 * e + 4] * f, o[8 * e + 5] * f);
+              u.w = pack_bf16(o[8 * e + 6] * f, o[8 * e + 7] * f);
+              dst[e] = u;
+            }
+          }
+        }
+        if (live && p.lse)
+          p.lse[(size_t)hg * p.pb.total_q + tok] =
+              (mlv.y > 0.f) ? (mlv.x * 0.6931471805599453f + logf(mlv.y)) : -INFINITY;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag) {
+    // a role gave up: the loads and MMAs still in flight land before the CTA
+    // frees its TMEM and exits
+    if (warp == 12 && lane == 0) {
+      drain_armed(&q_full[0], (armed_q + 1) / 2, never_flag);
+      drain_armed(&q_full[1], armed_q / 2, never_flag);
+      drain_armed(k_full, armed_k, never_flag);
+      drain_armed(v_full, armed_v, never_flag);
+    }
+    if (warp == 13 && lane == 0 && work) drain_mma(mma_drain, never_flag);  // MMAs may have been issued
+    __syncthreads();
+  }
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+}  // namespace mimo

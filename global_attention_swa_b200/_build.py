@@ -16,7 +16,8 @@ DEPS = [
     for f in ("mimo_attn.cu", "common.cuh", "decode_kernel.cuh", "prefill_kernel.cuh",
               "prefill_swa_kernel.cuh", "decode_fp8_kernel.cuh",
               "rope_append_kernel.cuh", "decode_merge_kernel.cuh",
-              "paged_common.cuh", "paged_attention_kernel.cuh", "paged_window_kernel.cuh", "paged_append_kernel.cuh",
+              "paged_common.cuh", "paged_attention_kernel.cuh", "paged_window_kernel.cuh", "paged_decode_kernel.cuh",
+              "paged_append_kernel.cuh",
               "page_table_kernel.cuh", "page_copy_kernel.cuh",
               "backward_kernel.cuh", "backward_tc_kernel.cuh", "backward_dq_tc_kernel.cuh")
 ] + [os.path.join(ROOT, "include", "mimo_attn.h")]

@@ -22,6 +22,7 @@
 #include "rope_append_kernel.cuh"
 #include "decode_merge_kernel.cuh"
 #include "paged_attention_kernel.cuh"
+#include "paged_decode_kernel.cuh"
 #include "paged_window_kernel.cuh"
 #include "paged_append_kernel.cuh"
 #include "page_table_kernel.cuh"
@@ -923,43 +924,59 @@ mimo::PagedBatch paged_batch(const int32_t* block_table, const int32_t* cu_seqle
   return b;
 }
 
-// Workspace of the paged attention: a descriptor per CTA and two slots of
-// partial results, tiles * 128 rows each (offsets from a 32-byte boundary).
+// Which kernel a call over a paged cache takes, by the most new tokens a
+// sequence brings and the G query heads of a key/value head.
+//   decode  at most 16 rows to a key/value head: warp-level MMAs, two CTAs to an SM
+//   window  all keys of one or two blocks of 128 / G tokens fit a score tile
+//   tile    one tile of 128 / G tokens, or two that share their key tiles
+struct PagedVariant {
+  enum Kind { decode, window, tile } kind;
+  int TQ;      // tokens of a tile of rows
+  int tiles;   // tiles (blocks) of an item
+  int rows;    // rows of a part in the workspace
+  bool split;  // items are cut and their parts joined
+  int ctas;    // of a full grid
+};
+// Under a short window an item has at most four key tiles (boxes of 16 keys:
+// the window, the item's other tokens and at most 15 keys before them), and
+// only whole items are dealt out: joining parts would cost more than the
+// shares' imbalance.
+constexpr int kPagedShortWindow = 512;
+PagedVariant paged_variant(const mimo_attn_dims_t* dims, int max_seqlen_q, int window) {
+  const int G = dims->num_heads_q / dims->num_heads_kv, sms = sm_count();
+  PagedVariant v;
+  v.TQ = 128 / G;
+  v.tiles = max_seqlen_q <= v.TQ ? 1 : 2;
+  v.kind = PagedVariant::tile;
+  v.ctas = sms;
+  const auto span = [&](int tiles) { return window - 1L + (long)tiles * v.TQ + mimo::kPwBoxRows - 1; };
+  if (G <= mimo::kPdRows && max_seqlen_q <= mimo::kPdRows / G) {
+    v.kind = PagedVariant::decode;
+    v.TQ = mimo::kPdRows / G;
+    v.tiles = 1;
+    v.ctas = 2 * sms;
+  } else if (window > 0 && span(1) <= mimo::kPwKeys) {
+    v.kind = PagedVariant::window;
+    if (span(v.tiles) > mimo::kPwKeys) v.tiles = 1;
+  }
+  v.rows = v.kind == PagedVariant::decode ? mimo::kPdRows : v.tiles * 128;
+  v.split = !(window > 0 && window <= kPagedShortWindow && (span(v.tiles) + mimo::kPgKeys - 1) / mimo::kPgKeys <= 4);
+  return v;
+}
+
+// Workspace of a call that cuts items: a descriptor per CTA and two slots of
+// partial results (offsets from a 32-byte boundary).
 struct PagedWorkspace {
   size_t off_ml, off_o, bytes;
 };
-PagedWorkspace paged_workspace(int tiles) {
-  PagedWorkspace w;
-  const size_t ctas = sm_count(), rows = ctas * 2 * tiles * 128;
+PagedWorkspace paged_workspace(const PagedVariant& v) {
+  PagedWorkspace w = {};
+  if (!v.split) return w;
+  const size_t ctas = v.ctas, rows = ctas * 2 * v.rows;
   w.off_ml = (ctas * sizeof(mimo::PgDesc) + 31) / 32 * 32;
   w.off_o = w.off_ml + rows * sizeof(float4);
   w.bytes = w.off_o + rows * 128 * sizeof(float) + 32;
   return w;
-}
-
-// Every sequence's new tokens fit one tile of rows.
-bool paged_one_tile(const mimo_attn_dims_t* dims, int max_seqlen_q) {
-  return max_seqlen_q <= 128 / (dims->num_heads_q / dims->num_heads_kv);
-}
-
-// Whether items are cut and their parts joined.  Under a short window an item
-// has at most four key tiles (boxes of 16 keys: the window, the block's other
-// tokens and at most 15 keys before them), and only whole items are dealt out:
-// joining parts would cost more than the shares' imbalance.
-constexpr int kPagedShortWindow = 512;
-bool paged_split(const mimo_attn_dims_t* dims, int tiles, int window) {
-  const long D = (long)tiles * (128 / (dims->num_heads_q / dims->num_heads_kv));
-  return !(window > 0 && window <= kPagedShortWindow && (window - 1L + D + 15 + 127) / 128 <= 4);
-}
-
-// Blocks of 128 / G tokens whose keys under this window, boxes of 16 and the
-// block's other tokens included, fit one score tile of the window kernel: 2, 1
-// or 0 (the general kernel).
-int paged_window_blocks(const mimo_attn_dims_t* dims, int tiles, int window) {
-  const long TQ = 128 / (dims->num_heads_q / dims->num_heads_kv);
-  for (int blocks = tiles; blocks >= 1; --blocks)
-    if (window > 0 && window - 1L + blocks * TQ + mimo::kPwBoxRows - 1 <= mimo::kPwKeys) return blocks;
-  return 0;
 }
 
 // Opt the paged attention into its dynamic shared memory once per device.
@@ -984,6 +1001,10 @@ mimo_status_t ensure_paged_attributes() {
   if ((st = cuda_check(cudaFuncSetAttribute(mimo::paged_window_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                             mimo::kPwSmemBytes),
                        "paged window smem attribute")))
+    return st;
+  if ((st = cuda_check(cudaFuncSetAttribute(mimo::paged_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            mimo::kPdSmemBytes),
+                       "paged decode smem attribute")))
     return st;
   done[dev].store(true, std::memory_order_release);
   return MIMO_OK;
@@ -1035,8 +1056,7 @@ size_t mimo_attn_paged_attention_workspace_size(const mimo_attn_dims_t* dims, in
   if (!dims || dims->num_heads_kv <= 0 || dims->num_heads_q < dims->num_heads_kv || num_seqs <= 0 ||
       total_q <= 0 || max_seqlen_q <= 0 || dims->num_heads_q / dims->num_heads_kv > 128)
     return 0;
-  const int tiles = paged_one_tile(dims, max_seqlen_q) ? 1 : 2;
-  return paged_split(dims, tiles, window) ? paged_workspace(tiles).bytes : 0;
+  return paged_workspace(paged_variant(dims, max_seqlen_q, window)).bytes;
 }
 
 mimo_status_t mimo_attn_paged_attention(const mimo_attn_dims_t* dims, const void* q, const void* k_pages,
@@ -1060,10 +1080,9 @@ mimo_status_t mimo_attn_paged_attention(const mimo_attn_dims_t* dims, const void
   if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) || !aligned4(lse) ||
       !aligned4(sinks))
     return fail(MIMO_ERR_INVALID_ARG, "q, k_pages, v_pages and out must be 16-byte aligned");
-  const int tiles = paged_one_tile(dims, max_seqlen_q) ? 1 : 2;
-  const PagedWorkspace ws = paged_workspace(tiles);
-  const bool split = paged_split(dims, tiles, window);
-  if (split && (!workspace || workspace_bytes < ws.bytes || !aligned16(workspace)))
+  const PagedVariant v = paged_variant(dims, max_seqlen_q, window);
+  const PagedWorkspace ws = paged_workspace(v);
+  if (v.split && (!workspace || workspace_bytes < ws.bytes || !aligned16(workspace)))
     return fail(MIMO_ERR_WORKSPACE, "workspace of %zu bytes, 16-byte aligned, is needed (got %zu)", ws.bytes,
                 workspace ? workspace_bytes : (size_t)0);
   if ((st = ensure_paged_attributes())) return st;
@@ -1081,17 +1100,15 @@ mimo_status_t mimo_attn_paged_attention(const mimo_attn_dims_t* dims, const void
   p.Hq = Hq;
   p.Hkv = Hkv;
   p.G = G;
-  p.TQ = 128 / G;
+  p.TQ = v.TQ;
   p.window = window;
   // Boxes: as many keys as divide both a page and a tile.  Under a short window
   // 16, so that an item reads few keys more than it sees.
-  int box = 128;
+  int box = v.kind == PagedVariant::decode ? mimo::kPdKeys : mimo::kPgKeys;
   while (page_size % box) box /= 2;
   if (window > 0 && window <= kPagedShortWindow) box = 16;
   p.box_rows = box;
-  p.split = split;
-  const int blocks = paged_window_blocks(dims, tiles, window);  // 0: the general kernel
-  const int D = (blocks ? blocks : tiles) * p.TQ;
+  p.split = v.split;
   p.min_tiles = 2;
   p.scale_log2 = scale_log2_of(dims);
   p.v_scale = v_scale_of(dims);
@@ -1099,7 +1116,7 @@ mimo_status_t mimo_attn_paged_attention(const mimo_attn_dims_t* dims, const void
   p.out_v8 = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
 
   CUtensorMap tq, tk, tv;
-  {
+  if (v.kind != PagedVariant::decode) {
     const uint64_t d[3] = {192, (uint64_t)Hq, (uint64_t)total_q};
     const uint64_t s[2] = {192 * 2, (uint64_t)Hq * 192 * 2};
     const uint32_t b[3] = {64, (uint32_t)G, (uint32_t)p.TQ};
@@ -1118,33 +1135,36 @@ mimo_status_t mimo_attn_paged_attention(const mimo_attn_dims_t* dims, const void
     if ((st = make_map(&tv, v_pages, 3, d, s, b))) return st;
   }
   // no more CTAs than items when only whole ones are dealt out; there are at
-  // most total_q / D + num_seqs blocks
-  const int ctas = p.split ? sm_count()
-                           : (int)std::min<long>(sm_count(), ((long)total_q / D + num_seqs) * Hkv);
-  if (blocks == 1)
-    mimo::paged_window_kernel<1><<<ctas, mimo::kPwThreads, mimo::kPwSmemBytes, (cudaStream_t)stream>>>(tq, tk, tv, p);
-  else if (blocks == 2)
-    mimo::paged_window_kernel<2><<<ctas, mimo::kPwThreads, mimo::kPwSmemBytes, (cudaStream_t)stream>>>(tq, tk, tv, p);
-  else if (tiles == 1)
-    mimo::paged_attention_kernel<1><<<ctas, mimo::kPgThreads, mimo::PgLayout<1>::kSmemBytes, (cudaStream_t)stream>>>(
-        tq, tk, tv, p);
+  // most total_q / D + num_seqs blocks of D tokens
+  const long items = ((long)total_q / (v.tiles * v.TQ) + num_seqs) * Hkv;
+  const int ctas = v.split ? v.ctas : (int)std::min<long>(v.ctas, items);
+  const cudaStream_t cs = (cudaStream_t)stream;
+  if (v.kind == PagedVariant::decode)
+    mimo::paged_decode_kernel<<<ctas, mimo::kPdThreads, mimo::kPdSmemBytes, cs>>>(
+        tk, tv, static_cast<const __nv_bfloat16*>(q), p);
+  else if (v.kind == PagedVariant::window && v.tiles == 1)
+    mimo::paged_window_kernel<1><<<ctas, mimo::kPwThreads, mimo::kPwSmemBytes, cs>>>(tq, tk, tv, p);
+  else if (v.kind == PagedVariant::window)
+    mimo::paged_window_kernel<2><<<ctas, mimo::kPwThreads, mimo::kPwSmemBytes, cs>>>(tq, tk, tv, p);
+  else if (v.tiles == 1)
+    mimo::paged_attention_kernel<1><<<ctas, mimo::kPgThreads, mimo::PgLayout<1>::kSmemBytes, cs>>>(tq, tk, tv, p);
   else
-    mimo::paged_attention_kernel<2><<<ctas, mimo::kPgThreads, mimo::PgLayout<2>::kSmemBytes, (cudaStream_t)stream>>>(
-        tq, tk, tv, p);
+    mimo::paged_attention_kernel<2><<<ctas, mimo::kPgThreads, mimo::PgLayout<2>::kSmemBytes, cs>>>(tq, tk, tv, p);
   if ((st = cuda_check(cudaGetLastError(), "paged attention launch"))) return st;
-  if (p.split) {
+  if (v.split) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas, tiles == 1 ? 4 : 8);
+    cfg.gridDim = dim3(ctas, v.rows <= 16 ? 2 : v.rows <= 128 ? 4 : 8);
     cfg.blockDim = dim3(256);
-    cfg.stream = (cudaStream_t)stream;
+    cfg.stream = cs;
     cudaLaunchAttribute at[1];  // the launch's own latency overlaps the kernel before it
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if ((st = cuda_check(cudaLaunchKernelEx(&cfg, tiles == 1 ? mimo::paged_combine_kernel<1> : mimo::paged_combine_kernel<2>, p),
-                         "paged combine launch")))
-      return st;
+    const auto combine = v.rows == mimo::kPdRows ? mimo::paged_combine_kernel<mimo::kPdRows>
+                         : v.rows == 128         ? mimo::paged_combine_kernel<128>
+                                                 : mimo::paged_combine_kernel<256>;
+    if ((st = cuda_check(cudaLaunchKernelEx(&cfg, combine, p), "paged combine launch"))) return st;
   }
   return ok();
 }

@@ -99,10 +99,12 @@ struct PgPlace {
   int b, g, i, t;
 };
 
-// Cost of an item of a sequence, in keys: what it reads.  In a window that is
-// the same for all blocks; without one, block i reads first + D (i + 1) keys
-// (first: the position of the chunk's first token, D: tokens of a block).
-// With whole items only, 1.
+// Cost of an item of a sequence, in keys: what it reads, and kPgItemCost for
+// its queries, its latencies and its epilogue (about what two key tiles take).
+// In a window that is the same for all blocks; without one, block i reads
+// first + D (i + 1) keys (first: the position of the chunk's first token, D:
+// tokens of a block).  With whole items only, 1.
+constexpr int kPgItemCost = 2 * kPgKeys;
 struct PgCost {
   long long base;  // block 0
   int slope;       // each further block
@@ -134,10 +136,10 @@ __device__ __forceinline__ PgCost pg_cost(const PagedAttnParams& p, const PagedS
     c.base = 1;
     c.slope = 0;
   } else if (p.window > 0) {
-    c.base = (long long)p.window + D;
+    c.base = (long long)p.window + D + kPgItemCost;
     c.slope = 0;
   } else {
-    c.base = (long long)(s.len - s.n) + D;
+    c.base = (long long)(s.len - s.n) + D + kPgItemCost;
     c.slope = D;
   }
   return c;
@@ -277,7 +279,7 @@ __device__ __forceinline__ bool pg_plan(const PagedAttnParams& p, PgPlace* plan,
       pl.g = (int)(y / group);
       y -= pl.g * group;
       pl.i = cost.block_of(y);
-      pl.t = p.split ? (int)((y - cost.upto(pl.i)) / kPgKeys) : 0;
+      pl.t = p.split ? (int)(max(0LL, y - cost.upto(pl.i) - kPgItemCost) / kPgKeys) : 0;
       plan[k] = pl;
       break;
     }
@@ -326,6 +328,11 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   long long* warp_sum = reinterpret_cast<long long*>(bars + 32);     // [12]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
   if (warp == 8) {
     if (lane == 0) {
       mbar_init(q_full, 1);
@@ -810,7 +817,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
 // where Z~ is Z over the parts' sums of the rounded P.  blockIdx.x: the CTA
 // whose share ends inside the item; its later parts are slot 0 of the CTAs
 // after it, up to the one where it ends.  One warp per row.
-template <int kTiles>
+template <int kRows>  // of a slot
 __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedAttnParams p) {
   const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // launched before the parts are complete
@@ -824,7 +831,6 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedAttnParam
     if (ends) last = k0 + __ffs(ends) - 1;
   }
   if (last < 0) return;  // a share gave up
-  constexpr int kRows = kTiles * 128;
   const int per_tile = p.TQ * p.G;  // valid rows of a full tile
   for (int v = blockIdx.y * 8 + warp; v < d.rows; v += gridDim.y * 8) {
     const int tile = v / per_tile, r = tile * 128 + (v - tile * per_tile);

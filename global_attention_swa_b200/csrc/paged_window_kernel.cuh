@@ -13,10 +13,11 @@
 // a pipeline over blocks: while one block's softmax runs, the next one's
 // scores are computed and the queries of the one after are on their way.
 //
-//   warp 12     loads: Q two buffers, a block ahead; K and V once per item,
-//               a lane per box of 16 keys (the page table is looked up here)
+//   warp 12     loads Q (two buffers, a block ahead) and K (once per item, a
+//               lane per box of 16 keys; the page table is looked up here)
 //   warp 13     MMA issuer: S(n) = Q K^T into score buffer n & 1, then O = P(n-1) V
-//   warp 14     zeroes the value rows that nothing of the item sees
+//   warp 14     loads V (once per item, as K) and zeroes the value rows that
+//               nothing of the item sees
 //   warps 0-7   softmax: warpgroup s takes the blocks with n & 1 == s, one row
 //               per thread, two passes over its TMEM row
 //   warps 8-11  epilogue: O / l -> out, lse
@@ -91,6 +92,11 @@ __global__ void __launch_bounds__(kPwThreads, 1)
   float4* ml = reinterpret_cast<float4*>(smem + kPwOffML);  // [2][128] (m, l, sink term) per row
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
   // phases armed: Q for blocks 0, 1, ... (buffer n & 1), K and V per item
   int armed_q = 0, armed_k = 0, armed_v = 0;
   for (int i = threadIdx.x; i < kPwKBox / 4; i += kPwThreads)
@@ -156,27 +162,18 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     int boxes = keys.n / kPwBoxRows;
     int row = have && lane < boxes ? pg_box_row(p, it, keys, lane) : 0;
     while (ok && have) {
-      const int nblk = blocks_of(it), bytes = boxes * kPwBoxRows * 128, row_now = row, boxes_now = boxes;
+      const int nblk = blocks_of(it), bytes = boxes * kPwBoxRows * 384, row_now = row, boxes_now = boxes;
       const int g = it.g;
       for (int blk = 0; ok && blk < nblk; ++blk, ++n) {
         if (blk == 0) {
           if (kp >= 1 && !(ok = wait_bounded(k_empty, (kp - 1) & 1, abort_flag))) break;
-          if (lane == 0) mbar_arrive_expect_tx(k_full, 3 * bytes);
+          if (lane == 0) mbar_arrive_expect_tx(k_full, bytes);
           ++armed_k;
           __syncwarp();
           if (lane < boxes_now) {
 #pragma unroll
             for (int c = 0; c < 3; ++c)
               tma_load_3d(smem + kPwOffK + c * kPwKBox + lane * kPwBoxRows * 128, &tm_k, k_full, c * 64, g, row_now);
-          }
-          if (kp >= 1 && !(ok = wait_bounded(v_empty, (kp - 1) & 1, abort_flag))) break;
-          if (lane == 0) mbar_arrive_expect_tx(v_full, 2 * bytes);
-          ++armed_v;
-          __syncwarp();
-          if (lane < boxes_now) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-              tma_load_3d(smem + kPwOffV + c * kPwKBox + lane * kPwBoxRows * 128, &tm_v, v_full, c * 64, g, row_now);
           }
           ++kp;
         }
@@ -250,11 +247,21 @@ __global__ void __launch_bounds__(kPwThreads, 1)
       if (ok && pm >= 0) do_pv(pm, pkp, pk, pfirst, plast);
     }
   } else if (warp == 14) {
-    // ------------------------------------------------------------ value rows nothing sees
+    // ------------------------------------------------------------ V, and its rows nothing sees
     int kp = 0;
     while (walk.next(p, it)) {
       const PgTile keys = pw_keys(it);
-      // not refilled before this item's P V, which waits for v_ready
+      const int boxes = keys.n / kPwBoxRows;
+      const int row = lane < boxes ? pg_box_row(p, it, keys, lane) : 0;
+      if (kp >= 1 && !wait_bounded(v_empty, (kp - 1) & 1, abort_flag)) break;
+      if (lane == 0) mbar_arrive_expect_tx(v_full, boxes * kPwBoxRows * 256);
+      ++armed_v;
+      __syncwarp();
+      if (lane < boxes) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          tma_load_3d(smem + kPwOffV + c * kPwKBox + lane * kPwBoxRows * 128, &tm_v, v_full, c * 64, it.g, row);
+      }
       if (!wait_bounded(v_full, kp & 1, abort_flag)) break;
       const int rows = keys.zlo + keys.n - keys.zhi;
       for (int w = lane; w < rows * 16; w += 32) {  // 16 vectors a row: 8 in each 64-column box
@@ -451,8 +458,8 @@ __global__ void __launch_bounds__(kPwThreads, 1)
       drain_armed(&q_full[0], (armed_q + 1) / 2, never_flag);
       drain_armed(&q_full[1], armed_q / 2, never_flag);
       drain_armed(k_full, armed_k, never_flag);
-      drain_armed(v_full, armed_v, never_flag);
     }
+    if (warp == 14 && lane == 0) drain_armed(v_full, armed_v, never_flag);
     if (warp == 13 && lane == 0 && work) drain_mma(mma_drain, never_flag);  // MMAs may have been issued
     __syncthreads();
   }

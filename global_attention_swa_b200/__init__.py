@@ -450,23 +450,24 @@ def _addr(t, name, dtype, shape, dev):
     words where something is wrong."""
     if t is None:
         return 0
-    if t.shape != shape:
-        _shape(t, shape, name)
-    if t.device != dev:
-        _same_device(dev, **{name: t})
-    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
-        return _ptr(t, name, dtype).value
-    return t.data_ptr()
+    if t.shape == shape and t.dtype is dtype and t.device == dev and t.is_contiguous() and t.is_cuda:
+        return t.data_ptr()
+    _shape(t, shape, name)
+    _same_device(dev, **{name: t})
+    return _ptr(t, name, dtype).value
 
 
 def _call(fn, dev, *args):
     """fn(*args, stream) with the tensors' device current; args[-1] is the caller's stream."""
-    args = (*args[:-1], _stream(args[-1], dev))
+    *args, stream = args
+    stream = _stream(stream, dev)
     if dev.type != "cuda" or torch.cuda.current_device() == dev.index:
-        _check(fn(*args))
+        status = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args))
+            status = fn(*args, stream)
+    if status:
+        _check(status)
 
 
 def _paged_pools(k_pages, v_pages, block_table):
@@ -505,20 +506,22 @@ def mimo_attn_paged_attention(q, k_pages, v_pages, block_table, cu_seqlens_q, se
              _addr(cu_seqlens_q, "cu_seqlens_q", _I32, (B + 1,), dev), _addr(seqlens, "seqlens", _I32, (B,), dev))
     sink = _addr(sinks, "sinks", _F32, (hq,), dev)
     if out is None:
-        out = torch.empty((nt, hq, dv), dtype=out_dtype, device=dev)
+        out = q.new_empty((nt, hq, dv), dtype=out_dtype)
     if lse is None and return_lse:
-        lse = torch.empty((hq, nt), dtype=torch.float32, device=dev)
+        lse = q.new_empty((hq, nt), dtype=_F32)
     max_seqlen_q, window = int(max_seqlen_q), int(window)
     dims = _dims_ref(hq, hkv, dqk, dv, softmax_scale, v_scale, out.dtype)
     need = lib.mimo_attn_paged_attention_workspace_size(dims, B, nt, max_seqlen_q, window)
-    if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws = wbytes = 0
+    if workspace is not None:
+        ws = _addr(workspace, "workspace", workspace.dtype, workspace.shape, dev)
+        wbytes = workspace.numel() * workspace.element_size()
+    elif need:
+        workspace, wbytes = block_table.new_empty(need + 3 >> 2), need
+        ws = workspace.data_ptr()
     _call(lib.mimo_attn_paged_attention, dev, dims, *addrs, B, nt, max_seqlen_q, P, ps, M, window, sink,
           _addr(out, "out", out.dtype if out.dtype in _OUT else _OUT, (nt, hq, dv), dev),
-          _addr(lse, "lse", _F32, (hq, nt), dev),
-          0 if workspace is None else _addr(workspace, "workspace", workspace.dtype, workspace.shape, dev),
-          wbytes, stream)
+          _addr(lse, "lse", _F32, (hq, nt), dev), ws, wbytes, stream)
     return out, lse
 
 
@@ -530,7 +533,7 @@ def mimo_attn_paged_append(q, k_new, v_new, k_pages, v_pages, block_table, cu_se
     P, ps, hkv, _, dv, B, M = _paged_pools(k_pages, v_pages, block_table)
     dev = q.device
     if q_out is None:
-        q_out = torch.empty((nt, hq, dqk), dtype=_BF16, device=dev)
+        q_out = q.new_empty((nt, hq, dqk))
     _call(lib.mimo_attn_paged_append, dev, _dims_ref(hq, hkv, dqk, dv),
           _addr(q, "q", _BF16, (nt, hq, dqk), dev), _addr(q_out, "q_out", _BF16, (nt, hq, dqk), dev),
           _addr(k_new, "k_new", _BF16, (nt, hkv, dqk), dev), _addr(v_new, "v_new", _BF16, (nt, hkv, dv), dev),
@@ -548,15 +551,12 @@ def _page_table(page_refs, block_table):
     return (page_refs.shape[0], *block_table.shape)
 
 
-def _ints(shape, dev):
-    return torch.empty(shape, dtype=_I32, device=dev)
-
-
-def _page_workspace(workspace, need, dev):
-    """(tensor, address, bytes) of the caller's workspace, or of a new one."""
+def _page_workspace(workspace, need, like):
+    """(tensor, address, bytes) of the caller's workspace, or of a new one beside ``like``."""
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    return (workspace, _addr(workspace, "workspace", workspace.dtype, workspace.shape, dev),
+        workspace = like.new_empty(need + 3 >> 2)
+        return workspace, workspace.data_ptr(), need
+    return (workspace, _addr(workspace, "workspace", workspace.dtype, workspace.shape, like.device),
             workspace.numel() * workspace.element_size())
 
 
@@ -572,11 +572,11 @@ def mimo_attn_page_hold(page_refs, block_table, seqlens, page_size, first=None, 
     """
     P, B, M = _page_table(page_refs, block_table)
     dev = page_refs.device
-    refs_out = _ints((P,), dev) if refs_out is None else refs_out
-    table_out = _ints((B, M), dev) if table_out is None else table_out
-    moves = _ints((B, 2), dev) if moves is None else moves
-    info = _ints((2,), dev) if info is None else info
-    ws, ws_addr, ws_bytes = _page_workspace(workspace, lib.mimo_attn_page_hold_workspace_size(P), dev)
+    refs_out = page_refs.new_empty((P,)) if refs_out is None else refs_out
+    table_out = page_refs.new_empty((B, M)) if table_out is None else table_out
+    moves = page_refs.new_empty((B, 2)) if moves is None else moves
+    info = page_refs.new_empty((2,)) if info is None else info
+    ws, ws_addr, ws_bytes = _page_workspace(workspace, lib.mimo_attn_page_hold_workspace_size(P), page_refs)
     _call(lib.mimo_attn_page_hold, dev, _addr(page_refs, "page_refs", _I32, (P,), dev), P,
           _addr(block_table, "block_table", _I32, (B, M), dev), B, M, int(page_size),
           _addr(seqlens, "seqlens", _I32, (B,), dev), _addr(first, "first", _I32, (B,), dev),
@@ -595,8 +595,8 @@ def mimo_attn_page_fork(page_refs, block_table, parent, refs_out=None, table_out
     P, B, M = _page_table(page_refs, block_table)
     n = parent.shape[0]
     dev = page_refs.device
-    refs_out = _ints((P,), dev) if refs_out is None else refs_out
-    table_out = _ints((n, M), dev) if table_out is None else table_out
+    refs_out = page_refs.new_empty((P,)) if refs_out is None else refs_out
+    table_out = page_refs.new_empty((n, M)) if table_out is None else table_out
     _call(lib.mimo_attn_page_fork, dev, _addr(page_refs, "page_refs", _I32, (P,), dev), P,
           _addr(block_table, "block_table", _I32, (B, M), dev), B, M, _addr(parent, "parent", _I32, (n,), dev), n,
           _addr(refs_out, "refs_out", _I32, (P,), dev), _addr(table_out, "table_out", _I32, (n, M), dev), stream)
@@ -614,11 +614,11 @@ def mimo_attn_page_compact(page_refs, block_table, max_moves, refs_out=None, tab
     P, B, M = _page_table(page_refs, block_table)
     max_moves = int(max_moves)
     dev = page_refs.device
-    refs_out = _ints((P,), dev) if refs_out is None else refs_out
-    table_out = _ints((B, M), dev) if table_out is None else table_out
-    moves = _ints((max_moves, 2), dev) if moves is None else moves
-    info = _ints((2,), dev) if info is None else info
-    ws, ws_addr, ws_bytes = _page_workspace(workspace, lib.mimo_attn_page_compact_workspace_size(P), dev)
+    refs_out = page_refs.new_empty((P,)) if refs_out is None else refs_out
+    table_out = page_refs.new_empty((B, M)) if table_out is None else table_out
+    moves = page_refs.new_empty((max_moves, 2)) if moves is None else moves
+    info = page_refs.new_empty((2,)) if info is None else info
+    ws, ws_addr, ws_bytes = _page_workspace(workspace, lib.mimo_attn_page_compact_workspace_size(P), page_refs)
     _call(lib.mimo_attn_page_compact, dev, _addr(page_refs, "page_refs", _I32, (P,), dev), P,
           _addr(block_table, "block_table", _I32, (B, M), dev), B, M, max_moves,
           _addr(refs_out, "refs_out", _I32, (P,), dev), _addr(table_out, "table_out", _I32, (B, M), dev),

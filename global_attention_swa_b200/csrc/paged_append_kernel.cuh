@@ -21,7 +21,8 @@
 namespace mimo {
 
 constexpr int kPaThreads = 256;
-constexpr int kPaBatch = 6;  // units in flight per thread: 64 heads' worth in a CTA
+constexpr int kPaPairs = 3;  // vectors in flight per thread: 64 heads' worth at rotary_dim 192,
+constexpr int kPaKept = 4;   // and at 64
 
 struct PagedAppendParams {
   PagedBatch pb;
@@ -36,42 +37,27 @@ struct PagedAppendParams {
   double inv_freq[kRaMaxHalf];  // theta^(-2 i / rotary_dim)
 };
 
-// The rows of one token in units of 16 bytes: `turn` pairs of vectors that
-// rotate into each other (dimensions 8j.. and half + 8j..), then `keep` vectors
-// that are copied (none where the destination is the source).
-struct PaRows {
-  int turn, keep, each;
-  uint32_t magic;  // w / each = w * magic >> 32 for w < 2^22
-  __device__ __forceinline__ PaRows(int half, bool in_place)
-      : turn(half / 8), keep(in_place ? 0 : 24 - 2 * (half / 8)), each(turn + keep) {
-    magic = each > 0 ? 0xffffffffu / each + 1 : 0;
-  }
+// A row of one token in 16-byte vectors: `turn` pairs of them rotate into each
+// other (dimensions 8j.. and half + 8j..), then `keep` are copied (none where
+// the destination is the source).
+struct PaSplit {
+  uint32_t each, magic;  // w / each = w * magic >> 32 for w < 2^22
+  __device__ __forceinline__ explicit PaSplit(int n) : each(n), magic(n > 1 ? 0xffffffffu / n + 1 : 0) {}
+  __device__ __forceinline__ int row(uint32_t w) const { return each == 1 ? (int)w : (int)__umulhi(w, magic); }
 };
-struct PaUnit {
+struct PaPair {
   uint4 a, b;
 };
-__device__ __forceinline__ void pa_place(const PaRows& s, int half, uint32_t w, int& row, int& j, int& x, int& y) {
-  row = s.each == 1 ? (int)w : (int)__umulhi(w, s.magic);
-  j = (int)w - row * s.each;
-  x = j < s.turn ? 8 * j : 2 * half + 8 * (j - s.turn);
-  y = j < s.turn ? half + 8 * j : -1;
-}
-__device__ __forceinline__ PaUnit pa_load(const PaRows& s, int half, const __nv_bfloat16* src, uint32_t w) {
-  int row, j, x, y;
-  pa_place(s, half, w, row, j, x, y);
-  PaUnit u;
-  u.a = *reinterpret_cast<const uint4*>(src + row * 192 + x);
-  u.b = y >= 0 ? *reinterpret_cast<const uint4*>(src + row * 192 + y) : make_uint4(0, 0, 0, 0);
+__device__ __forceinline__ PaPair pa_load(const PaSplit& s, int half, const __nv_bfloat16* src, uint32_t w) {
+  const int r = s.row(w), j = w - r * s.each;
+  PaPair u;
+  u.a = *reinterpret_cast<const uint4*>(src + r * 192 + 8 * j);
+  u.b = *reinterpret_cast<const uint4*>(src + r * 192 + half + 8 * j);
   return u;
 }
-__device__ __forceinline__ void pa_store(const PaRows& s, int half, __nv_bfloat16* dst, uint32_t w, const PaUnit& u,
+__device__ __forceinline__ void pa_store(const PaSplit& s, int half, __nv_bfloat16* dst, uint32_t w, const PaPair& u,
                                          const float2* cs) {
-  int row, j, x, y;
-  pa_place(s, half, w, row, j, x, y);
-  if (y < 0) {
-    *reinterpret_cast<uint4*>(dst + row * 192 + x) = u.a;
-    return;
-  }
+  const int r = s.row(w), j = w - r * s.each;
   const uint32_t av[4] = {u.a.x, u.a.y, u.a.z, u.a.w}, bv[4] = {u.b.x, u.b.y, u.b.z, u.b.w};
   uint32_t ra[4], rb[4];
 #pragma unroll
@@ -81,26 +67,37 @@ __device__ __forceinline__ void pa_store(const PaRows& s, int half, __nv_bfloat1
     ra[e] = pack_bf16(lo.x, hi.x);
     rb[e] = pack_bf16(lo.y, hi.y);
   }
-  *reinterpret_cast<uint4*>(dst + row * 192 + x) = make_uint4(ra[0], ra[1], ra[2], ra[3]);
-  *reinterpret_cast<uint4*>(dst + row * 192 + y) = make_uint4(rb[0], rb[1], rb[2], rb[3]);
+  *reinterpret_cast<uint4*>(dst + r * 192 + 8 * j) = make_uint4(ra[0], ra[1], ra[2], ra[3]);
+  *reinterpret_cast<uint4*>(dst + r * 192 + half + 8 * j) = make_uint4(rb[0], rb[1], rb[2], rb[3]);
+}
+// Offset of copied vector w of rows that keep s.each vectors from dimension 2 half on.
+__device__ __forceinline__ int pa_kept(const PaSplit& s, int half, uint32_t w) {
+  const int r = s.row(w);
+  return r * 192 + 2 * half + 8 * (w - r * s.each);
 }
 
-__global__ void __launch_bounds__(kPaThreads) paged_append_kernel(const PagedAppendParams p) {
+__global__ void __launch_bounds__(kPaThreads, 4) paged_append_kernel(const PagedAppendParams p) {
   __shared__ float2 cs[kRaMaxHalf];
   const int t = blockIdx.x;
   const int half = p.rotary_dim / 2;
   const bool vec = half % 8 == 0;
   const __nv_bfloat16* qs = p.q + (size_t)t * p.Hq * 192;
   __nv_bfloat16* qd = p.q_out + (size_t)t * p.Hq * 192;
-  const PaRows qr(half, p.q == p.q_out), kr(half, false);
-  const uint32_t qn = p.Hq * qr.each;
+  const PaSplit turn(half / 8), keep(24 - 2 * (half / 8));
+  const uint32_t qt = p.Hq * turn.each, qk = p.q == p.q_out ? 0 : p.Hq * keep.each;
   if (!MIMO_ROW_OK(t, p.pb.total_q)) return;
-  PaUnit u[kPaBatch];
+  PaPair u[kPaPairs];
+  uint4 c[kPaKept];
   if (vec) {
 #pragma unroll
-    for (int i = 0; i < kPaBatch; ++i) {
+    for (int i = 0; i < kPaPairs; ++i) {
       const uint32_t w = threadIdx.x + i * kPaThreads;
-      if (w < qn) u[i] = pa_load(qr, half, qs, w);
+      if (w < qt) u[i] = pa_load(turn, half, qs, w);
+    }
+#pragma unroll
+    for (int i = 0; i < kPaKept; ++i) {
+      const uint32_t w = threadIdx.x + i * kPaThreads;
+      if (w < qk) c[i] = *reinterpret_cast<const uint4*>(qs + pa_kept(keep, half, w));
     }
   }
   const int b = paged_seq_of_row(p.pb, t);  // the whole CTA takes the same branches
@@ -118,24 +115,35 @@ __global__ void __launch_bounds__(kPaThreads) paged_append_kernel(const PagedApp
     // the angle in double, reduced to [-pi, pi] before the fp32 sine and cosine
     const double a = (double)pos * p.inv_freq[threadIdx.x];
     const float r = (float)fma(-6.283185307179586476925286766559, rint(a * 0.15915494309189533576888376337251), a);
-    float sn, c;
-    sincosf(r, &sn, &c);
-    cs[threadIdx.x] = make_float2(c, sn);
+    float sn, co;
+    sincosf(r, &sn, &co);
+    cs[threadIdx.x] = make_float2(co, sn);
   }
   __syncthreads();
   const __nv_bfloat16* ks = p.k_new + (size_t)t * p.Hkv * 192;
   __nv_bfloat16* kd = p.k_pages + (kv ? slot : 0) * p.Hkv * 192;
   if (vec) {
 #pragma unroll
-    for (int i = 0; i < kPaBatch; ++i) {
+    for (int i = 0; i < kPaPairs; ++i) {
       const uint32_t w = threadIdx.x + i * kPaThreads;
-      if (w < qn) pa_store(qr, half, qd, w, u[i], cs);
+      if (w < qt) pa_store(turn, half, qd, w, u[i], cs);
     }
-    for (uint32_t w = threadIdx.x + kPaBatch * kPaThreads; w < qn; w += kPaThreads)
-      pa_store(qr, half, qd, w, pa_load(qr, half, qs, w), cs);
-    if (kv)
-      for (uint32_t w = threadIdx.x; w < (uint32_t)(p.Hkv * kr.each); w += kPaThreads)
-        pa_store(kr, half, kd, w, pa_load(kr, half, ks, w), cs);
+#pragma unroll
+    for (int i = 0; i < kPaKept; ++i) {
+      const uint32_t w = threadIdx.x + i * kPaThreads;
+      if (w < qk) *reinterpret_cast<uint4*>(qd + pa_kept(keep, half, w)) = c[i];
+    }
+    // what a CTA of this size does not hold at once
+    for (uint32_t w = threadIdx.x + kPaPairs * kPaThreads; w < qt; w += kPaThreads)
+      pa_store(turn, half, qd, w, pa_load(turn, half, qs, w), cs);
+    for (uint32_t w = threadIdx.x + kPaKept * kPaThreads; w < qk; w += kPaThreads)
+      *reinterpret_cast<uint4*>(qd + pa_kept(keep, half, w)) = *reinterpret_cast<const uint4*>(qs + pa_kept(keep, half, w));
+    if (kv) {
+      for (uint32_t w = threadIdx.x; w < p.Hkv * turn.each; w += kPaThreads)
+        pa_store(turn, half, kd, w, pa_load(turn, half, ks, w), cs);
+      for (uint32_t w = threadIdx.x; w < p.Hkv * keep.each; w += kPaThreads)
+        *reinterpret_cast<uint4*>(kd + pa_kept(keep, half, w)) = *reinterpret_cast<const uint4*>(ks + pa_kept(keep, half, w));
+    }
   } else {
     // a pair at a time
     const int rows = p.Hq + (kv ? p.Hkv : 0);

@@ -105,6 +105,13 @@ struct PgPlace {
 // first + D (i + 1) keys (first: the position of the chunk's first token, D:
 // tokens of a block).  With whole items only, 1.
 constexpr int kPgItemCost = 2 * kPgKeys;
+// Quotient of non-negative values; nearly always both fit 32 bits, and a 64-bit
+// division is a long chain of dependent instructions.
+__device__ __forceinline__ long long pg_div(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return (unsigned)a / (unsigned)b;
+  return a / b;
+}
+
 struct PgCost {
   long long base;  // block 0
   int slope;       // each further block
@@ -116,7 +123,7 @@ struct PgCost {
   __device__ __forceinline__ int block_of(long long y) const {
     int i;
     if (slope == 0) {
-      i = (int)(y / base);
+      i = (int)pg_div(y, base);
     } else {
       const double h = (double)base - 0.5 * slope;
       i = (int)((sqrt(h * h + 2.0 * slope * (double)y) - h) / slope);
@@ -155,6 +162,13 @@ struct PgItem {
   int start;        // first key of tile 0: lo rounded down to a box
   int n_kt;         // key tiles
   int t0, t1;       // the tiles of this share
+  int turn;         // the order of their passage: from t0 + turn on, then from t0
+  __device__ __forceinline__ int count() const { return t1 - t0; }
+  // The tile that passes j-th.
+  __device__ __forceinline__ int tile(int j) const {
+    const int t = t0 + turn + j;
+    return t < t1 ? t : t - (t1 - t0);
+  }
 };
 
 // Walks the items of a share.
@@ -164,6 +178,7 @@ struct PgWalk {
   PagedSeq s;
   int blocks;
   bool first;
+  int passed;  // tiles of this share in the items before
   __device__ __forceinline__ void seq(const PagedAttnParams& p) {
     const int D = kTiles * p.TQ;
     blocks = 0;
@@ -174,7 +189,7 @@ struct PgWalk {
       ++at.b;
     }
   }
-  __device__ __forceinline__ PgWalk(const PagedAttnParams& p, const PgPlace* plan) : at(plan[0]), end(plan[1]), first(true) {
+  __device__ __forceinline__ PgWalk(const PagedAttnParams& p, const PgPlace* plan) : at(plan[0]), end(plan[1]), first(true), passed(0) {
     seq(p);
   }
   // The next item with work in this share; false at its end.
@@ -208,7 +223,16 @@ struct PgWalk {
       it.n_kt = (it.hi - it.start) / kPgKeys + 1;
       it.t0 = at.t;
       it.t1 = last ? min(end.t, it.n_kt) : it.n_kt;
-      if (it.t0 < it.t1) return true;
+      if (it.t0 < it.t1) {
+        // All CTAs pass about as many tiles in a time, so the count so far is a
+        // clock they share: each begins an item at the tile the clock is at.  Those
+        // that work on blocks of one sequence then read the same keys at the same
+        // time, from L2, wherever their shares began.
+        const int at_clock = passed % it.n_kt;
+        it.turn = at_clock > it.t0 && at_clock < it.t1 ? at_clock - it.t0 : 0;
+        passed += it.t1 - it.t0;
+        return true;
+      }
     }
   }
 };
@@ -260,11 +284,11 @@ __device__ __forceinline__ bool pg_plan(const PagedAttnParams& p, PgPlace* plan,
   }
   before += incl - mine;
   const long long unit = p.split ? (long long)kPgKeys * p.min_tiles : 1;
-  const long long shares = max(1LL, min((long long)gridDim.x, total / unit));
+  const long long shares = max(1LL, min((long long)gridDim.x, pg_div(total, unit)));
   const int c = blockIdx.x;
 #pragma unroll 1
   for (int k = 0; k < 2; ++k) {
-    const long long x = total * min((long long)c + k, shares) / shares;
+    const long long x = pg_div(total * min((long long)c + k, shares), shares);
     if (x < before || x >= before + mine) continue;
     long long y = x - before;
     for (int b = b0; b < b1; ++b) {
@@ -276,7 +300,7 @@ __device__ __forceinline__ bool pg_plan(const PagedAttnParams& p, PgPlace* plan,
       }
       PgPlace pl;
       pl.b = b;
-      pl.g = (int)(y / group);
+      pl.g = (int)pg_div(y, group);
       y -= pl.g * group;
       pl.i = cost.block_of(y);
       pl.t = p.split ? (int)(max(0LL, y - cost.upto(pl.i) - kPgItemCost) / kPgKeys) : 0;
@@ -395,8 +419,8 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           }
         }
         ++n;
-        for (int t = it.t0; t < it.t1; ++t, ++kt) {
-          const PgTile tl = pg_tile(it, t);
+        for (int j = 0; j < it.count(); ++j, ++kt) {
+          const PgTile tl = pg_tile(it, it.tile(j));
           const int boxes = (tl.n + p.box_rows - 1) / p.box_rows;
           const int row = lane < boxes ? pg_box_row(p, it, tl, lane) : 0;
           const int ks = kt & 1;
@@ -423,8 +447,8 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       int kt = 0;
       bool ok = true;
       while (ok && walk.next(p, it)) {
-        for (int t = it.t0; t < it.t1; ++t, ++kt) {
-          const PgTile tl = pg_tile(it, t);
+        for (int j = 0; j < it.count(); ++j, ++kt) {
+          const PgTile tl = pg_tile(it, it.tile(j));
           const int boxes = (tl.n + p.box_rows - 1) / p.box_rows;
           const int row = lane < boxes ? pg_box_row(p, it, tl, lane) : 0;
           const int vs = kt % kVStages;
@@ -450,8 +474,8 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       int kt = 0;
       bool ok = true;
       while (ok && walk.next(p, it)) {
-        for (int t = it.t0; t < it.t1; ++t, ++kt) {
-          const PgTile tl = pg_tile(it, t);
+        for (int j = 0; j < it.count(); ++j, ++kt) {
+          const PgTile tl = pg_tile(it, it.tile(j));
           const int vs = kt % kVStages;
           // the stage is not refilled before this tile's P.V, which waits for v_ready
           if (!(ok = wait_bounded(&v_full[vs], (kt / kVStages) & 1, abort_flag))) break;
@@ -507,33 +531,33 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         if (!(ok = wait_bounded(q_full, n & 1, abort_flag))) break;
         if constexpr (kTiles == 1) {
           // scores run one key tile ahead of the softmax, in two TMEM buffers
-          auto scores = [&](int t, int kn) {
+          auto scores = [&](int j, int kn) {
             if (!wait_bounded(&k_full[kn & 1], (kn >> 1) & 1, abort_flag)) return false;
             tc_fence_after();
-            issue_s((kn & 1) ? tS1 : tS0, dQ0, kn & 1, pg_tile(it, t).n);
+            issue_s((kn & 1) ? tS1 : tS0, dQ0, kn & 1, pg_tile(it, it.tile(j)).n);
             umma_commit(&s_full[kn & 1]);
             umma_commit(&k_empty[kn & 1]);
-            if (t == it.t1 - 1) umma_commit(q_empty);
+            if (j == it.count() - 1) umma_commit(q_empty);
             return true;
           };
-          if (!(ok = scores(it.t0, kt))) break;
-          if (it.t0 + 1 < it.t1 && !(ok = scores(it.t0 + 1, kt + 1))) break;
-          for (int t = it.t0; t < it.t1; ++t, ++kt) {
-            const PgTile tl = pg_tile(it, t);
+          if (!(ok = scores(0, kt))) break;
+          if (it.count() > 1 && !(ok = scores(1, kt + 1))) break;
+          for (int j = 0; j < it.count(); ++j, ++kt) {
+            const int w = pg_tile(it, it.tile(j)).n;
             if (!(ok = wait_v())) break;
             if (!(ok = wait_bounded(&p_full[kt & 1], (kt >> 1) & 1, abort_flag))) break;
-            if (t == it.t0 && n > 0 && !(ok = wait_bounded(&o_empty[0], (n - 1) & 1, abort_flag))) break;
+            if (j == 0 && n > 0 && !(ok = wait_bounded(&o_empty[0], (n - 1) & 1, abort_flag))) break;
             tc_fence_after();
-            issue_pv(tO0, (kt & 1) ? tS1 : tS0, kt % kVStages, tl.n, t > it.t0);
+            issue_pv(tO0, (kt & 1) ? tS1 : tS0, kt % kVStages, w, j > 0);
             umma_commit(&v_empty[kt % kVStages]);
-            if (t == it.t1 - 1) umma_commit(&o_full[0]);
-            if (t + 2 < it.t1 && !(ok = scores(t + 2, kt + 2))) break;
+            if (j == it.count() - 1) umma_commit(&o_full[0]);
+            if (j + 2 < it.count() && !(ok = scores(j + 2, kt + 2))) break;
           }
         } else {
           if (!(ok = wait_bounded(&k_full[kt & 1], (kt >> 1) & 1, abort_flag))) break;
           tc_fence_after();
           {
-            const int w = pg_tile(it, it.t0).n;
+            const int w = pg_tile(it, it.tile(0)).n;
             issue_s(tS0, dQ0, kt & 1, w);
             umma_commit(&s_full[0]);
             if (has1) {
@@ -541,18 +565,17 @@ __global__ void __launch_bounds__(kPgThreads, 1)
               umma_commit(&s_full[1]);
             }
             umma_commit(&k_empty[kt & 1]);
-            if (it.t1 - it.t0 == 1) umma_commit(q_empty);
+            if (it.count() == 1) umma_commit(q_empty);
           }
-          for (int t = it.t0; t < it.t1; ++t, ++kt) {
-            const bool last = t == it.t1 - 1;
-            const PgTile tl = pg_tile(it, t);
-            const int wn = last ? 0 : pg_tile(it, t + 1).n;
+          for (int j = 0; j < it.count(); ++j, ++kt) {
+            const bool last = j == it.count() - 1;
+            const int w = pg_tile(it, it.tile(j)).n, wn = last ? 0 : pg_tile(it, it.tile(j + 1)).n;
             if (!(ok = wait_v())) break;
             if (!(ok = wait_bounded(&p_full[0], c0 & 1, abort_flag))) break;
             // O_0 is free once the previous item's epilogue has read it
-            if (t == it.t0 && n > 0 && !(ok = wait_bounded(&o_empty[0], (n - 1) & 1, abort_flag))) break;
+            if (j == 0 && n > 0 && !(ok = wait_bounded(&o_empty[0], (n - 1) & 1, abort_flag))) break;
             tc_fence_after();
-            issue_pv(tO0, tS0, 0, tl.n, t > it.t0);
+            issue_pv(tO0, tS0, 0, w, j > 0);
             ++c0;
             if (last) umma_commit(&o_full[0]);
             const int kn = kt + 1;
@@ -561,13 +584,13 @@ __global__ void __launch_bounds__(kPgThreads, 1)
               tc_fence_after();
               issue_s(tS0, dQ0, kn & 1, wn);
               umma_commit(&s_full[0]);
-              if (!has1 && t + 1 == it.t1 - 1) umma_commit(q_empty);
+              if (!has1 && j + 1 == it.count() - 1) umma_commit(q_empty);
             }
             if (has1) {
               if (!(ok = wait_bounded(&p_full[1], c1 & 1, abort_flag))) break;
-              if (t == it.t0 && n1 > 0 && !(ok = wait_bounded(&o_empty[1], (n1 - 1) & 1, abort_flag))) break;
+              if (j == 0 && n1 > 0 && !(ok = wait_bounded(&o_empty[1], (n1 - 1) & 1, abort_flag))) break;
               tc_fence_after();
-              issue_pv(tO1, tS1, 0, tl.n, t > it.t0);
+              issue_pv(tO1, tS1, 0, w, j > 0);
               ++c1;
               if (last) umma_commit(&o_full[1]);
             }
@@ -576,7 +599,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
               if (has1) {
                 issue_s(tS1, dQ1, kn & 1, wn);
                 umma_commit(&s_full[1]);
-                if (t + 1 == it.t1 - 1) umma_commit(q_empty);
+                if (j + 1 == it.count() - 1) umma_commit(q_empty);
               }
               umma_commit(&k_empty[kn & 1]);
             }
@@ -624,14 +647,14 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       float m = sunk ? p.sinks[h] * 1.4426950408889634f : row_ok ? -INFINITY : 0.f;
       float l = sunk ? 1.f : 0.f;  // exact row sum (lse)
       float lr = l;                // sum of the bf16-rounded P that enter P.V (output)
-      for (int t = it.t0; t < it.t1; ++t, ++tg) {
+      for (int j = 0; j < it.count(); ++j, ++tg) {
         const int buf = kTiles == 1 ? (tg & 1) : i;
         const int phase = kTiles == 1 ? (tg >> 1) & 1 : tg & 1;
         const uint32_t tS = tbase + lane_off + buf * 128;
         if (!(ok = wait_bounded(&s_full[buf], phase, abort_flag))) break;
         tc_fence_after();
         if (warp_ok) {
-          const int kpos0 = it.start + t * kPgKeys;
+          const int kpos0 = it.start + it.tile(j) * kPgKeys;
           float s[128];
           tmem_load128_sync(tS, s);
           const bool full_tile = kpos0 + kPgKeys - 1 <= pos0 &&
@@ -661,7 +684,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
               l *= alpha;
               lr *= alpha;
               m = m_new;
-              rescale_o = t > it.t0;
+              rescale_o = j > 0;
             }
             if (__any_sync(0xffffffffu, rescale_o)) {
               // O must hold the previous key tile's product: with two tiles S(t) was

@@ -21,9 +21,9 @@
 //
 //   warp 8      loads Q and K (TMA), allocates TMEM
 //   warp 9      issues the MMAs (one thread): S = Q K^T (SS), O += P V (TS, P from TMEM)
-//   warp 10     loads V (TMA)
-//   warp 11     zeroes the value rows of a key tile that the item does not see
-//               (they may hold anything, and 0 * NaN would reach the sum)
+//   warp 10     loads V (TMA) and zeroes the value rows of a key tile that the
+//               item does not see (they may hold anything, and 0 * NaN would
+//               reach the sum); warp 11 completes the warpgroup
 //   warps 0-3   softmax and epilogue of tile 0 (one row per thread)
 //   warps 4-7   softmax and epilogue of tile 1
 //
@@ -241,6 +241,7 @@ struct PgWalk {
 // of 16), and the rows [0, zlo) and [zhi, n) that nothing of the item sees.
 struct PgTile {
   int k0, n, zlo, zhi;
+  __device__ __forceinline__ bool edge() const { return zlo > 0 || zhi < n; }
 };
 __device__ __forceinline__ PgTile pg_tile(const PgItem& it, int t) {
   PgTile r;
@@ -338,7 +339,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   uint64_t* k_empty = bars + 4;   // [2]
   uint64_t* v_full = bars + 6;    // [kVStages]
   uint64_t* v_empty = bars + 8;   // [kVStages]
-  uint64_t* v_ready = bars + 10;  // [kVStages] once warp 11 has zeroed a tile's unseen rows
+  uint64_t* v_ready = bars + 10;  // [kVStages] the unseen rows of an edge tile are zeroed
   uint64_t* s_full = bars + 12;   // [2] two tiles: of tile i; one: of key tile parity i
   uint64_t* p_full = bars + 14;   // [2]
   uint64_t* o_full = bars + 16;   // [2]
@@ -463,31 +464,18 @@ __global__ void __launch_bounds__(kPgThreads, 1)
 #pragma unroll
             for (int c = 0; c < 2; ++c) tma_load_3d(dst + c * 16384, &tm_v, &v_full[vs], c * 64, it.g, row);
           }
-        }
-      }
-    }
-  } else if (warp == 11) {
-    // ------------------------------------------------------------ value rows nothing sees
-    if (work) {
-      PgWalk<kTiles> walk(p, plan);
-      PgItem it;
-      int kt = 0;
-      bool ok = true;
-      while (ok && walk.next(p, it)) {
-        for (int j = 0; j < it.count(); ++j, ++kt) {
-          const PgTile tl = pg_tile(it, it.tile(j));
-          const int vs = kt % kVStages;
-          // the stage is not refilled before this tile's P.V, which waits for v_ready
-          if (!(ok = wait_bounded(&v_full[vs], (kt / kVStages) & 1, abort_flag))) break;
-          uint8_t* vb = smem + Lay::kOffV + vs * kPgVBytes;
-          const int rows = tl.zlo + tl.n - tl.zhi;
-          for (int w = lane; w < rows * 16; w += 32) {  // 16 vectors a row: 8 in each 64-column box
-            const int i = w >> 4, r = i < tl.zlo ? i : tl.zhi + (i - tl.zlo);
-            *reinterpret_cast<uint4*>(vb + ((w >> 3) & 1) * 16384 + r * 128 + (w & 7) * 16) = make_uint4(0, 0, 0, 0);
+          if (tl.edge()) {  // at most two tiles of an item
+            if (!(ok = wait_bounded(&v_full[vs], (kt / kVStages) & 1, abort_flag))) break;
+            uint8_t* vb = smem + Lay::kOffV + vs * kPgVBytes;
+            const int rows = tl.zlo + tl.n - tl.zhi;
+            for (int w = lane; w < rows * 16; w += 32) {  // 16 vectors a row: 8 in each 64-column box
+              const int i = w >> 4, r = i < tl.zlo ? i : tl.zhi + (i - tl.zlo);
+              *reinterpret_cast<uint4*>(vb + ((w >> 3) & 1) * 16384 + r * 128 + (w & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&v_ready[vs]);
           }
-          if (rows > 0) fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&v_ready[vs]);
         }
       }
     }
@@ -525,7 +513,14 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       int kt = 0;          // key tiles (all items): K and V phases
       int c0 = 0, c1 = 0;  // score tiles of tile 0 / 1: s_full, p_full phases (two tiles)
       bool ok = true;
-      auto wait_v = [&]() { return wait_bounded(&v_ready[kt % kVStages], (kt / kVStages) & 1, abort_flag); };
+      uint32_t edges = 0;  // parity of each stage's edge tiles: v_ready phases
+      // (a stage's next tile is loaded after this one's P.V, so neither wait can fall behind)
+      auto wait_v = [&](bool edge) {
+        const int vs = kt % kVStages;
+        if (!edge) return wait_bounded(&v_full[vs], (kt / kVStages) & 1, abort_flag);
+        edges ^= 1u << vs;
+        return wait_bounded(&v_ready[vs], ~(edges >> vs) & 1, abort_flag);
+      };
       while (ok && walk.next(p, it)) {
         const bool has1 = kTiles == 2 && it.tokens > p.TQ;
         if (!(ok = wait_bounded(q_full, n & 1, abort_flag))) break;
@@ -543,8 +538,9 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           if (!(ok = scores(0, kt))) break;
           if (it.count() > 1 && !(ok = scores(1, kt + 1))) break;
           for (int j = 0; j < it.count(); ++j, ++kt) {
-            const int w = pg_tile(it, it.tile(j)).n;
-            if (!(ok = wait_v())) break;
+            const PgTile tl = pg_tile(it, it.tile(j));
+            const int w = tl.n;
+            if (!(ok = wait_v(tl.edge()))) break;
             if (!(ok = wait_bounded(&p_full[kt & 1], (kt >> 1) & 1, abort_flag))) break;
             if (j == 0 && n > 0 && !(ok = wait_bounded(&o_empty[0], (n - 1) & 1, abort_flag))) break;
             tc_fence_after();
@@ -569,8 +565,9 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           }
           for (int j = 0; j < it.count(); ++j, ++kt) {
             const bool last = j == it.count() - 1;
-            const int w = pg_tile(it, it.tile(j)).n, wn = last ? 0 : pg_tile(it, it.tile(j + 1)).n;
-            if (!(ok = wait_v())) break;
+            const PgTile tl = pg_tile(it, it.tile(j));
+            const int w = tl.n, wn = last ? 0 : pg_tile(it, it.tile(j + 1)).n;
+            if (!(ok = wait_v(tl.edge()))) break;
             if (!(ok = wait_bounded(&p_full[0], c0 & 1, abort_flag))) break;
             // O_0 is free once the previous item's epilogue has read it
             if (j == 0 && n > 0 && !(ok = wait_bounded(&o_empty[0], (n - 1) & 1, abort_flag))) break;
@@ -609,7 +606,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         if (has1) ++n1;
       }
     }
-  } else {
+  } else if (warp < 8) {
     // ------------------------------------------------------------ softmax / epilogue
     setmaxnreg_inc<200>();
     const int i = warp >> 2;          // which tile

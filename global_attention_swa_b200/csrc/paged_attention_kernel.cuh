@@ -60,7 +60,8 @@ struct PgLayout {
   static constexpr int kOffK = kTiles * kPgQBytes;
   static constexpr int kOffV = kOffK + kPgKStages * kPgKBytes;
   static constexpr int kOffBar = kOffV + kVStages * kPgVBytes;
-  static constexpr int kSmemBytes = kOffBar + 512 + 1024;  // barriers, plan; alignment slack
+  static constexpr int kOffItems = kOffBar + 384;             // barriers and plan before it
+  static constexpr int kSmemBytes = kOffItems + 8 * 128 + 1024;  // a walk and item per softmax warp; alignment slack
 };
 
 // Partial results in the workspace: one descriptor per CTA, then for each CTA
@@ -192,6 +193,7 @@ struct PgWalk {
   __device__ __forceinline__ PgWalk(const PagedAttnParams& p, const PgPlace* plan) : at(plan[0]), end(plan[1]), first(true), passed(0) {
     seq(p);
   }
+  __device__ __forceinline__ PgWalk() {}
   // The next item with work in this share; false at its end.
   __device__ __forceinline__ bool next(const PagedAttnParams& p, PgItem& it) {
     while (true) {
@@ -406,7 +408,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       int n = 0, kt = 0;  // items and key tiles loaded
       bool ok = true;
       while (ok && walk.next(p, it)) {
-        if (n > 0 && !(ok = wait_bounded(q_empty, (n - 1) & 1, abort_flag))) break;
+        if (n > 0 && !(ok = wait_warp(q_empty, (n - 1) & 1, abort_flag))) break;
         const bool has1 = kTiles == 2 && it.tokens > p.TQ;
         if (lane == 0) {
           const int bytes = p.TQ * p.G * 384;
@@ -425,7 +427,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           const int boxes = (tl.n + p.box_rows - 1) / p.box_rows;
           const int row = lane < boxes ? pg_box_row(p, it, tl, lane) : 0;
           const int ks = kt & 1;
-          if (kt >= 2 && !(ok = wait_bounded(&k_empty[ks], ((kt >> 1) - 1) & 1, abort_flag))) break;
+          if (kt >= 2 && !(ok = wait_warp(&k_empty[ks], ((kt >> 1) - 1) & 1, abort_flag))) break;
           if (lane == 0) {
             mbar_arrive_expect_tx(&k_full[ks], boxes * p.box_rows * 384);
             armed[1] = kt + 1;
@@ -453,7 +455,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           const int boxes = (tl.n + p.box_rows - 1) / p.box_rows;
           const int row = lane < boxes ? pg_box_row(p, it, tl, lane) : 0;
           const int vs = kt % kVStages;
-          if (kt >= kVStages && !(ok = wait_bounded(&v_empty[vs], (kt / kVStages - 1) & 1, abort_flag))) break;
+          if (kt >= kVStages && !(ok = wait_warp(&v_empty[vs], (kt / kVStages - 1) & 1, abort_flag))) break;
           if (lane == 0) {
             mbar_arrive_expect_tx(&v_full[vs], boxes * p.box_rows * 256);
             armed[2] = kt + 1;
@@ -465,7 +467,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
             for (int c = 0; c < 2; ++c) tma_load_3d(dst + c * 16384, &tm_v, &v_full[vs], c * 64, it.g, row);
           }
           if (tl.edge()) {  // at most two tiles of an item
-            if (!(ok = wait_bounded(&v_full[vs], (kt / kVStages) & 1, abort_flag))) break;
+            if (!(ok = wait_warp(&v_full[vs], (kt / kVStages) & 1, abort_flag))) break;
             uint8_t* vb = smem + Lay::kOffV + vs * kPgVBytes;
             const int rows = tl.zlo + tl.n - tl.zhi;
             for (int w = lane; w < rows * 16; w += 32) {  // 16 vectors a row: 8 in each 64-column box
@@ -617,9 +619,22 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     int n = 0;   // items this tile slot took part in
     int tg = 0;  // score tiles it consumed
     bool ok = true;
-    PgWalk<kTiles> walk(p, plan);
-    PgItem it;
-    while (ok && work && (kTiles == 2 || i == 0) && walk.next(p, it)) {
+    // The walk and the item live in shared memory, one copy per warp: the loop
+    // over key tiles needs every register.
+    struct Items {
+      PgWalk<kTiles> walk;
+      PgItem it;
+    };
+    static_assert(sizeof(Items) <= 128, "one slot per warp");
+    Items& items = *reinterpret_cast<Items*>(smem + Lay::kOffItems + warp * 128);
+    if (lane == 0) items.walk = PgWalk<kTiles>(p, plan);
+    const auto next = [&]() {  // by one lane for the warp
+      __syncwarp();
+      const int more = lane == 0 ? items.walk.next(p, items.it) : 0;
+      return __shfl_sync(0xffffffffu, more, 0) != 0;  // the item is visible after it
+    };
+    const PgItem& it = items.it;
+    while (ok && work && (kTiles == 2 || i == 0) && next()) {
       const int tokens = min(p.TQ, it.tokens - i * p.TQ);  // valid tokens of this tile
       const bool whole = it.t0 == 0 && it.t1 == it.n_kt;
       if (threadIdx.x == 0 && !whole) {
@@ -644,14 +659,16 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       float m = sunk ? p.sinks[h] * 1.4426950408889634f : row_ok ? -INFINITY : 0.f;
       float l = sunk ? 1.f : 0.f;  // exact row sum (lse)
       float lr = l;                // sum of the bf16-rounded P that enter P.V (output)
-      for (int j = 0; j < it.count(); ++j, ++tg) {
+      const int wrap = it.start + it.t1 * kPgKeys, span = it.count() * kPgKeys;
+      int kpos0 = it.start + it.tile(0) * kPgKeys;  // first key of the tile
+      bool later = false;                           // not the first tile to pass
+      for (int j = it.count(); j > 0; --j, ++tg, later = true) {
         const int buf = kTiles == 1 ? (tg & 1) : i;
         const int phase = kTiles == 1 ? (tg >> 1) & 1 : tg & 1;
         const uint32_t tS = tbase + lane_off + buf * 128;
         if (!(ok = wait_bounded(&s_full[buf], phase, abort_flag))) break;
         tc_fence_after();
         if (warp_ok) {
-          const int kpos0 = it.start + it.tile(j) * kPgKeys;
           float s[128];
           tmem_load128_sync(tS, s);
           const bool full_tile = kpos0 + kPgKeys - 1 <= pos0 &&
@@ -681,7 +698,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
               l *= alpha;
               lr *= alpha;
               m = m_new;
-              rescale_o = j > 0;
+              rescale_o = later;
             }
             if (__any_sync(0xffffffffu, rescale_o)) {
               // O must hold the previous key tile's product: with two tiles S(t) was
@@ -741,6 +758,8 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         }
         tc_fence_before();
         mbar_arrive(&p_full[buf]);
+        kpos0 += kPgKeys;
+        if (kpos0 == wrap) kpos0 -= span;
       }
       if (!ok) break;
       // ---------------- epilogue: O is read out of TMEM first and released, so

@@ -39,6 +39,15 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedBatch& p, int b) {
   return s;
 }
 
+// wait_bounded for a whole warp, polled by its first lane alone: each lane's poll
+// is a shared-memory operation of its own, and 32 of them from a warp with
+// nothing else to do take bandwidth from the operands of the tensor cores.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  int ok = 1;
+  if ((threadIdx.x & 31) == 0) ok = wait_bounded(bar, parity, abort);
+  return __shfl_sync(0xffffffffu, ok, 0);
+}
+
 // The sequence of packed row t, found by the whole warp: how many sequences
 // end at or before t (32 of cu_q at a time, 32 runs of it first); -1 for a row
 // that none owns.  For a sound cu_q that is the sequence with cu_q[b] <= t <

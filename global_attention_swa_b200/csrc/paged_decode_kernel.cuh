@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kPdThreads, 2)
     bool ok = true;
     while (ok && walk.next(p, it)) {
       const int qb = n & 1;
-      if (n >= 2 && !(ok = wait_bounded(&q_empty[qb], ((n >> 1) - 1) & 1, abort_flag))) break;
+      if (n >= 2 && !(ok = wait_warp(&q_empty[qb], ((n >> 1) - 1) & 1, abort_flag))) break;
       const int rows = it.tokens * p.G;
       if (lane == 0) mbar_arrive_expect_tx(&q_full[qb], rows * 384);
       __syncwarp();
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kPdThreads, 2)
         tl.k0 = k0;
         const int row = lane < boxes ? pg_box_row(p, it, tl, lane) : 0;
         const int st = kt & 1;
-        if (kt >= kPdStages && !(ok = wait_bounded(&empty[st], ((kt >> 1) - 1) & 1, abort_flag))) break;
+        if (kt >= kPdStages && !(ok = wait_warp(&empty[st], ((kt >> 1) - 1) & 1, abort_flag))) break;
         if (lane == 0) mbar_arrive_expect_tx(&full[st], boxes * p.box_rows * 640);
         __syncwarp();
         if (lane < boxes) {

@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
       const int g = it.g;
       for (int blk = 0; ok && blk < nblk; ++blk, ++n) {
         if (blk == 0) {
-          if (kp >= 1 && !(ok = wait_bounded(k_empty, (kp - 1) & 1, abort_flag))) break;
+          if (kp >= 1 && !(ok = wait_warp(k_empty, (kp - 1) & 1, abort_flag))) break;
           if (lane == 0) mbar_arrive_expect_tx(k_full, bytes);
           ++armed_k;
           __syncwarp();
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
           boxes = keys.n / kPwBoxRows;
           row = lane < boxes ? pg_box_row(p, it, keys, lane) : 0;
         }
-        if (n + 1 >= 2 && !(ok = wait_bounded(&q_empty[bn], (((n + 1) >> 1) - 1) & 1, abort_flag))) break;
+        if (n + 1 >= 2 && !(ok = wait_warp(&q_empty[bn], (((n + 1) >> 1) - 1) & 1, abort_flag))) break;
         load_q(it, in_item ? blk + 1 : 0, bn);
       }
     }
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
       const PgTile keys = pw_keys(it);
       const int boxes = keys.n / kPwBoxRows;
       const int row = lane < boxes ? pg_box_row(p, it, keys, lane) : 0;
-      if (kp >= 1 && !wait_bounded(v_empty, (kp - 1) & 1, abort_flag)) break;
+      if (kp >= 1 && !wait_warp(v_empty, (kp - 1) & 1, abort_flag)) break;
       if (lane == 0) mbar_arrive_expect_tx(v_full, boxes * kPwBoxRows * 256);
       ++armed_v;
       __syncwarp();
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         for (int c = 0; c < 2; ++c)
           tma_load_3d(smem + kPwOffV + c * kPwKBox + lane * kPwBoxRows * 128, &tm_v, v_full, c * 64, it.g, row);
       }
-      if (!wait_bounded(v_full, kp & 1, abort_flag)) break;
+      if (!wait_warp(v_full, kp & 1, abort_flag)) break;
       const int rows = keys.zlo + keys.n - keys.zhi;
       for (int w = lane; w < rows * 16; w += 32) {  // 16 vectors a row: 8 in each 64-column box
         const int i = w >> 4, r = i < keys.zlo ? i : keys.zhi + (i - keys.zlo);

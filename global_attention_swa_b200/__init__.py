@@ -441,6 +441,29 @@ def mimo_attn_prefill_backward(q, k, v, out, lse, dout, sinks, window, cu_seqlen
     return dq, dk, dv, ds
 
 
+def _load_fast():
+    """The native part of the binding (csrc/fast_call.cpp) on the loaded library, or None
+    where it was not built: the calls then go through the marshalling below."""
+    try:
+        from . import _fast_call
+    except ImportError:
+        return None
+    _fast_call.bind(*(ctypes.cast(getattr(lib, f"mimo_attn_{name}"), ctypes.c_void_p).value for name in (
+        "paged_attention", "paged_attention_workspace_size", "paged_append", "page_hold",
+        "page_hold_workspace_size", "page_fork", "page_compact", "page_compact_workspace_size", "page_copy")))
+    return _fast_call
+
+
+_fast = _load_fast()
+
+
+def _taken(r):
+    """The result of a native call: its tensors, or the error its status stands for."""
+    if r.__class__ is int:
+        _check(r)
+    return r
+
+
 _dims_ref = functools.lru_cache(maxsize=256)(lambda *args: ctypes.byref(make_dims(*args)))
 
 
@@ -497,6 +520,12 @@ def mimo_attn_paged_attention(q, k_pages, v_pages, block_table, cu_seqlens_q, se
 
     Returns (out [Nt,Hq,128], lse [Hq,Nt] fp32 or None).
     """
+    if _fast is not None and stream is None:
+        r = _fast.paged_attention(q, k_pages, v_pages, block_table, cu_seqlens_q, seqlens, max_seqlen_q, window,
+                                  sinks, out, lse, workspace, (out_dtype if out is None else out.dtype) is _F32,
+                                  0.0 if softmax_scale is None else softmax_scale, v_scale, return_lse)
+        if r is not None:
+            return _taken(r)
     nt, hq, dqk = q.shape
     P, ps, hkv, _, dv, B, M = _paged_pools(k_pages, v_pages, block_table)
     dev = q.device
@@ -529,6 +558,11 @@ def mimo_attn_paged_append(q, k_new, v_new, k_pages, v_pages, block_table, cu_se
                            rope_theta, rotary_dim=None, q_out=None, stream=None):
     """Rotate the new tokens' q and k and write k, v into their pages (see
     include/mimo_attn.h).  Returns the rotated q: ``q_out`` (which may be q), or a new tensor."""
+    if _fast is not None and stream is None:
+        r = _fast.paged_append(q, k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q, seqlens, rope_theta,
+                               q.shape[-1] if rotary_dim is None else rotary_dim, q_out)
+        if r is not None:
+            return _taken(r)
     nt, hq, dqk = q.shape
     P, ps, hkv, _, dv, B, M = _paged_pools(k_pages, v_pages, block_table)
     dev = q.device
@@ -570,6 +604,11 @@ def mimo_attn_page_hold(page_refs, block_table, seqlens, page_size, first=None, 
     Returns (refs_out, table_out, moves [B,2] for mimo_attn_page_copy, info [2]: pages
     missing (nothing was changed if > 0), pages free afterwards).
     """
+    if _fast is not None and stream is None:
+        r = _fast.page_hold(page_refs, block_table, seqlens, page_size, first, write_from, refs_out, table_out, moves,
+                            info, workspace)
+        if r is not None:
+            return _taken(r)
     P, B, M = _page_table(page_refs, block_table)
     dev = page_refs.device
     refs_out = page_refs.new_empty((P,)) if refs_out is None else refs_out
@@ -590,6 +629,10 @@ def mimo_attn_page_fork(page_refs, block_table, parent, refs_out=None, table_out
     """Row i of the new table is row parent[i] of block_table, empty where parent[i] < 0
     (see include/mimo_attn.h).  refs_out may be page_refs (in place); table_out may not
     be block_table.  Returns (refs_out, table_out)."""
+    if _fast is not None and stream is None:
+        r = _fast.page_fork(page_refs, block_table, parent, refs_out, table_out)
+        if r is not None:
+            return _taken(r)
     if parent.dim() != 1:
         raise ValueError("parent must be 1-D")
     P, B, M = _page_table(page_refs, block_table)
@@ -611,6 +654,10 @@ def mimo_attn_page_compact(page_refs, block_table, max_moves, refs_out=None, tab
     Returns (refs_out, table_out, moves [max_moves,2] for mimo_attn_page_copy, info [2]:
     moves made, pages in use).
     """
+    if _fast is not None and stream is None:
+        r = _fast.page_compact(page_refs, block_table, max_moves, refs_out, table_out, moves, info, workspace)
+        if r is not None:
+            return _taken(r)
     P, B, M = _page_table(page_refs, block_table)
     max_moves = int(max_moves)
     dev = page_refs.device
@@ -631,6 +678,10 @@ def mimo_attn_page_copy(k_pages, v_pages, moves, stream=None):
     """Copy pages moves[:, 0] over pages moves[:, 1] in place (rows of -1 are skipped; see
     include/mimo_attn.h).  k_pages / v_pages [P,page_size,Hkv,192/128] bf16 of one layer, or
     [layers,P,...] of several.  Returns (k_pages, v_pages)."""
+    if _fast is not None and stream is None:
+        r = _fast.page_copy(k_pages, v_pages, moves)
+        if r is not None:
+            return _taken(r)
     if k_pages.dim() not in (4, 5) or k_pages.dim() != v_pages.dim():
         raise ValueError("k_pages and v_pages must be [num_pages, page_size, Hkv, D], or with a layer axis first")
     shape = k_pages.shape

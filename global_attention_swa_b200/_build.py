@@ -1,4 +1,5 @@
-"""Builds ``libmimo_attn.so`` in-tree with nvcc for sm_100a."""
+"""Builds ``libmimo_attn.so`` in-tree with nvcc for sm_100a, and the native part of
+the Python binding (``_fast_call``) with the host compiler."""
 
 from __future__ import annotations
 
@@ -60,7 +61,41 @@ def build(force=False, verbose=False, checked=False):
     return lib
 
 
+FAST_SRC = os.path.join(PKG, "csrc", "fast_call.cpp")
+
+
+def fast_call_path():
+    import sysconfig
+
+    return os.path.join(PKG, "_fast_call" + sysconfig.get_config_var("EXT_SUFFIX"))
+
+
+def build_fast_call(force=False):
+    """Compile the binding's native calls against the installed torch if their source is
+    newer than them; returns the .so path."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    so = fast_call_path()
+    deps = (FAST_SRC, os.path.join(ROOT, "include", "mimo_attn.h"))
+    if not force and os.path.exists(so) and all(os.path.getmtime(d) <= os.path.getmtime(so) for d in deps):
+        return so
+    include = [*cpp_extension.include_paths("cuda"), sysconfig.get_paths()["include"]]
+    libs = cpp_extension.library_paths("cuda")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-I{d}" for d in include), FAST_SRC, "-o", so, *(f"-L{d}" for d in libs),
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("the binding's native calls failed to compile:\n" + res.stdout + res.stderr)
+    return so
+
+
 if __name__ == "__main__":
     import sys
 
     build(force=True, verbose=True, checked="--checked" in sys.argv)
+    build_fast_call()

@@ -282,3 +282,26 @@ def test_paged_cache_refuses_sizes():
     for bad in (dict(num_pages=0), dict(page_size=24), dict(window=-1), dict(rollback=-1), dict(num_layers=0)):
         with pytest.raises(ValueError):
             PagedCache(**{**dict(num_layers=1, num_pages=4, page_size=16, num_seqs=2, max_pages=2, device="cpu"), **bad})
+
+
+def test_native_calls_leave_what_is_not_plain_to_the_binding():
+    """Host tensors, wrong counts of arguments and things that are no tensors: the native
+    part of the binding says None, and the wrapper goes on to say what is wrong."""
+    if mimo._fast is None:
+        pytest.skip("the native part of the binding is not built")
+    x = _inputs()
+    args = (x["q"], x["kp"], x["vp"], x["table"], x["cu"], x["lens"], 5, 0, x["sinks"], None, None, None, False, 0.0,
+            1.0, True)
+    assert mimo._fast.paged_attention(*args) is None
+    assert mimo._fast.paged_attention(*args[:-1]) is None
+    assert mimo._fast.paged_attention(None, *args[1:]) is None
+    assert mimo._fast.page_hold(x["refs"], x["table"], x["lens"], 16, *[None] * 7) is None
+    assert mimo._fast.page_fork(x["refs"], x["table"], x["lens"], None, None) is None
+    assert mimo._fast.page_compact(x["refs"], x["table"], 3, *[None] * 5) is None
+    assert mimo._fast.page_copy(x["kp"], x["vp"], torch.zeros((1, 2), dtype=I32)) is None
+    assert mimo._fast.paged_append(x["q"], x["k"], x["v"], x["kp"], x["vp"], x["table"], x["cu"], x["lens"], 1e4, 192,
+                                   None) is None
+    with pytest.raises(TypeError):
+        mimo._fast.bind(1, 2)
+    with pytest.raises(ValueError, match="CUDA"):
+        _call_hold(x)

@@ -519,6 +519,65 @@ def test_copy(layers, pool, ps, hkv):
     assert torch.equal(k.cpu(), kp) and torch.equal(v.cpu(), vp)
 
 
+# ------------------------------------------------------------------ the binding's two ways
+
+
+def test_native_calls_and_marshalling_give_the_same(monkeypatch):
+    """Every call through the native part of the binding and through Python's own
+    marshalling: the same outputs, the same refusals."""
+    assert mimo._fast is not None, "the native part of the binding is not built: run __graft_entry__.build()"
+    x = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in build([90, 40], [20, 3], 0, 16, 16, 1, 2).items()}
+    refs, table, lens = (ints(v).cuda() for v in _state(1, 40, 7, 5, 16))
+    g = torch.Generator(device="cuda").manual_seed(0)
+    k, v = (torch.randn((23, 1, d), generator=g, device="cuda").bfloat16() for d in (192, 128))
+
+    def calls(native):
+        taken = []
+        if native:
+            spy = type("Spy", (), {n: staticmethod(lambda *a, f=getattr(real, n): taken.append(f(*a)) or taken[-1])
+                                   for n in dir(real) if not n.startswith("_")})
+            monkeypatch.setattr(mimo, "_fast", spy)
+        else:
+            monkeypatch.setattr(mimo, "_fast", None)
+        kp, vp = x["kp"].clone(), x["vp"].clone()
+        out = torch.empty((23, 16, 128), device="cuda")
+        args = (x["q"], kp, vp, x["table"], x["cu"], x["lens"], x["most"])
+        got = [*mimo.mimo_attn_paged_attention(*args, 0, x["sinks"]),
+               *mimo.mimo_attn_paged_attention(*args, 129, None, out=out, softmax_scale=0.1, v_scale=0.7, return_lse=False),
+               *mimo.mimo_attn_paged_attention(*args, 0, x["sinks"], out_dtype=torch.float32,
+                                               workspace=torch.empty(1 << 26, dtype=torch.uint8, device="cuda")),
+               mimo.mimo_attn_paged_append(x["q"], k, v, kp, vp, x["table"], x["cu"], x["lens"], 1e4),
+               mimo.mimo_attn_paged_append(x["q"], k, v, kp, vp, x["table"], x["cu"], x["lens"], 1e4, 64,
+                                           q_out=torch.empty_like(x["q"])),
+               *mimo.mimo_attn_page_hold(refs, table, lens, 16, first=lens // 2, write_from=lens),
+               *mimo.mimo_attn_page_fork(refs, table, lens % 7), *mimo.mimo_attn_page_compact(refs, table, 3),
+               *mimo.mimo_attn_page_copy(kp, vp, ints([[0, 1], [-1, -1]]).cuda())]
+        mimo.mimo_attn_device_status()
+        said = []
+        for bad in (lambda: mimo.mimo_attn_paged_attention(x["q"].half(), *args[1:], 0, x["sinks"]),
+                    lambda: mimo.mimo_attn_paged_attention(x["q"], kp[:, :8], *args[2:], 0, x["sinks"]),
+                    lambda: mimo.mimo_attn_paged_attention(*args, -1, x["sinks"]),
+                    lambda: mimo.mimo_attn_paged_attention(*args[:4], x["cu"].cpu(), *args[5:], 0, x["sinks"]),
+                    lambda: mimo.mimo_attn_paged_attention(*args, 0, x["sinks"], workspace=torch.empty(8, device="cuda")),
+                    lambda: mimo.mimo_attn_paged_append(x["q"], k, v, kp, vp, x["table"], x["cu"], x["lens"], 1e4, 7),
+                    lambda: mimo.mimo_attn_page_hold(refs, table, lens[:3], 16),
+                    lambda: mimo.mimo_attn_page_fork(refs, table, ints([0]).cuda(), table_out=table[:1]),
+                    lambda: mimo.mimo_attn_page_compact(refs, table, -1),
+                    lambda: mimo.mimo_attn_page_copy(kp, vp, torch.zeros((2, 2), device="cuda"))):
+            with pytest.raises((ValueError, TypeError, RuntimeError)) as e:
+                bad()
+            said.append((type(e.value), str(e.value)))
+        return got, said, taken
+
+    real = mimo._fast
+    a, said_a, taken = calls(True)
+    assert sum(r is not None for r in taken) >= 9  # the native calls did run
+    b, said_b, _ = calls(False)
+    assert said_a == said_b
+    for p, q in zip(a, b):
+        assert (p is None and q is None) or (p.dtype == q.dtype and torch.equal(p.nan_to_num(), q.nan_to_num()))
+
+
 # ------------------------------------------------------------------ a run of them together
 
 

@@ -1028,9 +1028,18 @@ mimo_status_t check_page_table(const int32_t* page_refs, int num_pages, const in
 }
 
 // One cluster of CTAs over `elements` array elements: enough that each thread
-// passes over a few, at most the portable cluster size.
-template <typename Params>
+// passes over a few.
+template <typename Params>  // each kernel has its own: `done` is the kernel's
 mimo_status_t launch_cluster(void (*kernel)(Params), const Params& p, long elements, void* stream, const char* what) {
+  static std::atomic<bool> done[64];  // per device: clusters past the portable size are allowed
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return fail(MIMO_ERR_CUDA, "cudaGetDevice failed");
+  if (!done[dev].load(std::memory_order_acquire)) {
+    const mimo_status_t st =
+        cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1), what);
+    if (st) return st;
+    done[dev].store(true, std::memory_order_release);
+  }
   int ctas = 1;
   while (ctas < mimo::kPtMaxCtas && elements > (long)ctas * 2 * mimo::kPtThreads) ctas *= 2;
   cudaLaunchConfig_t cfg = {};

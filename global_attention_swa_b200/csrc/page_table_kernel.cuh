@@ -22,7 +22,7 @@ namespace mimo {
 
 constexpr int kPtThreads = 1024;
 constexpr int kPtWarps = kPtThreads / 32;
-constexpr int kPtMaxCtas = 8;       // portable cluster size
+constexpr int kPtMaxCtas = 16;      // a cluster of 16 is past the portable size: opted into at the first launch
 constexpr int kPtForkRows = 2048;   // table rows of one histogram round
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -276,28 +276,36 @@ __global__ void __launch_bounds__(kPtThreads, 1) page_hold_kernel(const PageHold
   if (touched) {
     rank = off.before[0];
     HoldCursor c(p, entries.begin + lane);
-    for (int i0 = entries.begin; i0 < entries.end; i0 += 32) {
-      const int i = i0 + lane;
-      const bool in = i < entries.end && c.row.ok;
-      const int v = in ? p.table_out[i] : 0;
-      const bool take = in && (v <= -2 || (v == -1 && c.wanted()));
-      const uint32_t f = __ballot_sync(0xffffffffu, take);
-      if (take) {
-        const int pg = __ldcg(&p.ws[1 + rank + __popc(f & ((1u << lane) - 1))]);
-        p.table_out[i] = pg;
-        p.refs_out[pg] = 1;
-        if (v <= -2) {
-          if (atomicSub(&p.refs_out[-2 - v], 1) == 1) atomicAdd(&p.ws[0], 1);
-          if ((long long)c.j * p.page_size < c.row.write_from) {  // at most one page of a sequence
-            p.moves[2 * c.b] = -2 - v;
-            p.moves[2 * c.b + 1] = pg;
-          }
-        }
-      } else if (in && v >= 0 && !c.wanted()) {
-        p.table_out[i] = -1;
+    for (int i0 = entries.begin; i0 < entries.end; i0 += 32 * kPtBatch) {
+      int w[kPtBatch];
+#pragma unroll
+      for (int u = 0; u < kPtBatch; ++u) {
+        const int i = i0 + 32 * u + lane;
+        w[u] = i < entries.end ? p.table_out[i] : 0;
       }
-      rank += __popc(f);
-      c.step(p);
+#pragma unroll
+      for (int u = 0; u < kPtBatch; ++u) {
+        const int i = i0 + 32 * u + lane, v = w[u];
+        const bool in = i < entries.end && c.row.ok;
+        const bool take = in && (v <= -2 || (v == -1 && c.wanted()));
+        const uint32_t f = __ballot_sync(0xffffffffu, take);
+        if (take) {
+          const int pg = __ldcg(&p.ws[1 + rank + __popc(f & ((1u << lane) - 1))]);
+          p.table_out[i] = pg;
+          p.refs_out[pg] = 1;
+          if (v <= -2) {
+            if (atomicSub(&p.refs_out[-2 - v], 1) == 1) atomicAdd(&p.ws[0], 1);
+            if ((long long)c.j * p.page_size < c.row.write_from) {  // at most one page of a sequence
+              p.moves[2 * c.b] = -2 - v;
+              p.moves[2 * c.b + 1] = pg;
+            }
+          }
+        } else if (in && v >= 0 && !c.wanted()) {
+          p.table_out[i] = -1;
+        }
+        rank += __popc(f);
+        c.step(p);
+      }
     }
   }
   cluster_sync_all();

@@ -876,26 +876,46 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedAttnParam
     const int tok = d.row0 + v / p.G, h = d.h0 + v % p.G;
     if (!MIMO_ROW_OK((long long)tok * p.Hq + h, (long long)p.pb.total_q * p.Hq)) continue;
     const float sg = p.sinks ? p.sinks[h] * 1.4426950408889634f : -INFINITY;
+    // a lane holds the statistics of one part; further parts come in rounds of 32
+    const auto row_of = [&](int k) { return ((size_t)k * 2 + (k == c)) * kRows + r; };
     float M = sg;
-    for (int k = c; k <= last; ++k)
-      M = fmaxf(M, p.ws_ml[((size_t)k * 2 + (k == c)) * kRows + r].x);
+    float4 ml = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+    for (int k0 = c; k0 <= last; k0 += 32) {
+      if (k0 + lane <= last) {
+        ml = p.ws_ml[row_of(k0 + lane)];
+        M = fmaxf(M, ml.x);
+      }
+    }
+#pragma unroll
+    for (int e = 16; e > 0; e >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, e));
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float Z = 0.f, Zr = 0.f;
     if (M != -INFINITY) {
-      Z = (sg == -INFINITY) ? 0.f : ex2(sg - M);
-      Zr = Z;
-      for (int k = c; k <= last; ++k) {
-        const size_t row = ((size_t)k * 2 + (k == c)) * kRows + r;
-        const float4 ml = p.ws_ml[row];
+      const bool one_round = last - c < 32;
+      for (int k0 = c; k0 <= last; k0 += 32) {
+        const int parts = min(32, last + 1 - k0);
+        if (!one_round) ml = lane < parts ? p.ws_ml[row_of(k0 + lane)] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
         const float w = (ml.x == -INFINITY) ? 0.f : ex2(ml.x - M);
         Z += w * ml.y;
         Zr += w * ml.z;
-        const float4 o = reinterpret_cast<const float4*>(p.ws_o + row * 128)[lane];
-        acc.x += w * o.x;
-        acc.y += w * o.y;
-        acc.z += w * o.z;
-        acc.w += w * o.w;
+#pragma unroll 4
+        for (int e = 0; e < parts; ++e) {
+          const float we = __shfl_sync(0xffffffffu, w, e);
+          const float4 o = reinterpret_cast<const float4*>(p.ws_o + row_of(k0 + e) * 128)[lane];
+          acc.x += we * o.x;
+          acc.y += we * o.y;
+          acc.z += we * o.z;
+          acc.w += we * o.w;
+        }
       }
+#pragma unroll
+      for (int e = 16; e > 0; e >>= 1) {
+        Z += __shfl_xor_sync(0xffffffffu, Z, e);
+        Zr += __shfl_xor_sync(0xffffffffu, Zr, e);
+      }
+      const float ps = (sg == -INFINITY) ? 0.f : ex2(sg - M);
+      Z += ps;
+      Zr += ps;
     }
     const float f = (Zr > 0.f) ? p.v_scale / Zr : 0.f;
     const size_t ob = ((size_t)tok * p.Hq + h) * 32 + lane;

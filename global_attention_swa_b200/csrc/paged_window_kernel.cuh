@@ -300,77 +300,69 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         if (!(ok = wait_bounded(&s_full[b], (n >> 1) & 1, abort_flag))) break;
         tc_fence_after();
         const uint32_t tS = tbase + lane_off + b * kPwKeys;
-        float m = sg2;
-        float2 l2 = make_float2(0.f, 0.f);
+        float m = sg2, l = 0.f;
         if (warp_ok) {
-          // pass 1: row max over the visible columns, 48 at a time; columns at or
-          // past N lie outside [c_lo, c_hi] and are masked like the window's edges
+          // Rows go by token, so a warp's masks lie between its first and its last
+          // row's: a run of 16 columns is visible to all rows, to none, or masked, and
+          // the warp takes one way.
+          const int lo_min = __shfl_sync(0xffffffffu, c_lo, 0), lo_max = __shfl_sync(0xffffffffu, c_lo, 31);
+          const int hi_min = __shfl_sync(0xffffffffu, c_hi, 0), hi_max = __shfl_sync(0xffffffffu, c_hi, 31);
+          const auto all_see = [&](int c) { return c >= lo_max && c + 15 <= hi_min; };
+          const auto none_sees = [&](int c) { return c > hi_max || c + 15 < lo_min; };
+          // pass 1: row max over the visible columns (those at or past N are masked)
           float mx0 = -INFINITY, mx1 = -INFINITY;
-          for (int c0 = 0; c0 < N; c0 += 48) {
-            uint32_t v[48];
-            tmem_load48_sync(tS + c0, v);
+#pragma unroll 1
+          for (int c0 = 0; c0 < N; c0 += 32) {
+            uint32_t v[32];
+            tmem_load32_sync(tS + c0, v);
 #pragma unroll
-            for (int q = 0; q < 3; ++q) {
+            for (int q = 0; q < 2; ++q) {
               const int cq0 = c0 + 16 * q;
-              if (cq0 >= c_lo && cq0 + 15 <= c_hi) {
+              if (all_see(cq0)) {
 #pragma unroll
                 for (int e = 0; e < 16; e += 4) {
                   mx0 = fmax3(mx0, __uint_as_float(v[16 * q + e]), __uint_as_float(v[16 * q + e + 1]));
                   mx1 = fmax3(mx1, __uint_as_float(v[16 * q + e + 2]), __uint_as_float(v[16 * q + e + 3]));
                 }
-              } else {
+              } else if (!none_sees(cq0)) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                  const int c = cq0 + e;
-                  if (c >= c_lo && c <= c_hi) mx0 = fmaxf(mx0, __uint_as_float(v[16 * q + e]));
-                }
+                for (int e = 0; e < 16; ++e)
+                  mx0 = fmaxf(mx0, cq0 + e >= c_lo && cq0 + e <= c_hi ? __uint_as_float(v[16 * q + e]) : -INFINITY);
               }
             }
           }
           m = fmaxf(sg2, fmaxf(mx0, mx1) * p.scale_log2);
           const float neg_m = (m == -INFINITY) ? 0.f : -m;
           // pass 2: P = 2^(s*scale - m) (0 outside the window), bf16 over the same
-          // columns (P of columns [c0, c0 + 48) lands in [c0 / 2, c0 / 2 + 24), behind
+          // columns (P of columns [c0, c0 + 32) lands in [c0 / 2, c0 / 2 + 16), behind
           // the read position); the unrounded sum gives lse
-          for (int c0 = 0; c0 < N; c0 += 48) {
-            uint32_t v[48];
-            tmem_load48_sync(tS + c0, v);
+          float2 l2 = make_float2(0.f, 0.f);
+          const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(neg_m, neg_m);
+#pragma unroll 1
+          for (int c0 = 0; c0 < N; c0 += 32) {
+            uint32_t v[32], pk[16];
+            tmem_load32_sync(tS + c0, v);
+            if (!(all_see(c0) && all_see(c0 + 16))) {
 #pragma unroll
-            for (int q = 0; q < 3; ++q) {
-              const int cq0 = c0 + 16 * q;
-              uint32_t pk[8];
-              if (cq0 >= c_lo && cq0 + 15 <= c_hi) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const float2 x =
-                      fma2(make_float2(__uint_as_float(v[16 * q + 2 * e]), __uint_as_float(v[16 * q + 2 * e + 1])),
-                           make_float2(p.scale_log2, p.scale_log2), make_float2(neg_m, neg_m));
-                  const float2 pe = make_float2(ex2(x.x), ex2(x.y));
-                  pk[e] = pack_bf16(pe.x, pe.y);
-                  l2 = add2(l2, pe);
-                }
-              } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const int c = cq0 + 2 * e;
-                  const float x0 = fmaf(__uint_as_float(v[16 * q + 2 * e]), p.scale_log2, neg_m);
-                  const float x1 = fmaf(__uint_as_float(v[16 * q + 2 * e + 1]), p.scale_log2, neg_m);
-                  const float2 pe = make_float2((c >= c_lo && c <= c_hi) ? ex2(x0) : 0.f,
-                                                (c + 1 >= c_lo && c + 1 <= c_hi) ? ex2(x1) : 0.f);
-                  pk[e] = pack_bf16(pe.x, pe.y);
-                  l2 = add2(l2, pe);
-                }
-              }
-              if (cq0 < N) tmem_st8(tS + cq0 / 2, pk);
+              for (int e = 0; e < 32; ++e) v[e] = c0 + e >= c_lo && c0 + e <= c_hi ? v[e] : 0xff800000u;  // -inf
             }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float2 y = fma2(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), sc2, nm2);
+              const float2 pe = make_float2(ex2(y.x), ex2(y.y));
+              pk[e] = pack_bf16(pe.x, pe.y);
+              l2 = add2(l2, pe);
+            }
+            tmem_st16(tS + c0 / 2, pk);
           }
+          l = l2.x + l2.y;
           tmem_wait_st();
         }
         tc_fence_before();
         mbar_arrive(&p_full[b]);
         const float ps = (sg2 != -INFINITY) ? ex2(sg2 - m) : 0.f;  // the sink's term
         if (n >= 2 && !(ok = wait_bounded(&ml_empty[b], ((n >> 1) - 1) & 1, abort_flag))) break;
-        ml[b * 128 + r] = make_float4(m, l2.x + l2.y + ps, ps, 0.f);
+        ml[b * 128 + r] = make_float4(m, l + ps, ps, 0.f);
         mbar_arrive(&ml_full[b]);
       }
     }

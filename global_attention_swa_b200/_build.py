@@ -87,7 +87,7 @@ def build_fast_call(force=False):
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *(f"-I{d}" for d in include), FAST_SRC, "-o", so, *(f"-L{d}" for d in libs),
-           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError("the binding's native calls failed to compile:\n" + res.stdout + res.stderr)

@@ -12,6 +12,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -45,6 +46,10 @@ struct Args {
   bool plain = true;
   c10::Device dev{c10::kCPU};
 
+  // at::empty without its dispatch.
+  at::Tensor empty(Sizes sizes, c10::ScalarType type) const {
+    return at::Tensor(at::detail::empty_cuda(sizes, type, dev, std::nullopt));
+  }
   // A tensor that must be there; the first one sets the device.
   const at::Tensor* tensor(int i) {
     if (!plain || !THPVariable_Check(a[i])) {
@@ -80,7 +85,7 @@ struct Args {
       t = *x;
       return check(t, type, sizes);
     }
-    t = at::empty(sizes, at::TensorOptions().dtype(type).device(dev));
+    t = empty(sizes, type);
     return t.data_ptr();
   }
   // The caller's workspace, or a new one of `need` bytes.
@@ -98,7 +103,7 @@ struct Args {
       return t.data_ptr();
     }
     if (!need) return nullptr;
-    t = at::empty({(int64_t)need}, at::TensorOptions().dtype(at::kByte).device(dev));
+    t = empty({(int64_t)need}, at::kByte);
     bytes = need;
     return t.data_ptr();
   }

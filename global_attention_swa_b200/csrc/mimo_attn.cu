@@ -1162,7 +1162,7 @@ mimo_status_t mimo_attn_paged_attention(const mimo_attn_dims_t* dims, const void
   if ((st = cuda_check(cudaGetLastError(), "paged attention launch"))) return st;
   if (v.split) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas, v.rows <= 16 ? 2 : v.rows <= 128 ? 4 : 8);
+    cfg.gridDim = dim3(ctas, v.rows / 8);  // a warp to a row: each is a chain of dependent loads
     cfg.blockDim = dim3(256);
     cfg.stream = cs;
     cudaLaunchAttribute at[1];  // the launch's own latency overlaps the kernel before it

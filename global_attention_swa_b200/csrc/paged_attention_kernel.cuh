@@ -122,12 +122,13 @@ struct PgCost {
   }
   // the block that holds cost y of [0, upto(blocks))
   __device__ __forceinline__ int block_of(long long y) const {
+    if (blocks <= 1) return 0;
     int i;
     if (slope == 0) {
       i = (int)pg_div(y, base);
-    } else {
-      const double h = (double)base - 0.5 * slope;
-      i = (int)((sqrt(h * h + 2.0 * slope * (double)y) - h) / slope);
+    } else {  // the root of upto(i) = y, near enough for the steps below to find it
+      const float h = (float)base - 0.5f * slope, z = 2.f * (float)y;
+      i = (int)(z / (sqrtf(h * h + slope * z) + h));
     }
     i = max(0, min(i, blocks - 1));
     while (i > 0 && upto(i) > y) --i;
@@ -861,20 +862,26 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedAttnParam
   const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // launched before the parts are complete
   if (timed_out_before()) return;  // after a recorded timeout: write nothing
+  // both loads at once: this CTA's descriptor, and whether the item ends in one of the next 32
+  int k = c + 1 + lane;
+  int open0 = k < (int)gridDim.x ? p.ws_desc[k].open0 : 0;
   const PgDesc d = p.ws_desc[c];
   if (!d.open1) return;
   int last = -1;  // the CTA where the item ends
-  for (int k0 = c + 1; k0 < (int)gridDim.x && last < 0; k0 += 32) {
-    const int k = k0 + lane;
-    const uint32_t ends = __ballot_sync(0xffffffffu, k < (int)gridDim.x && p.ws_desc[k].open0 == 2);
+  for (int k0 = c + 1;; k0 += 32) {
+    const uint32_t ends = __ballot_sync(0xffffffffu, open0 == 2);
     if (ends) last = k0 + __ffs(ends) - 1;
+    if (last >= 0 || k0 + 32 >= (int)gridDim.x) break;
+    k = k0 + 32 + lane;
+    open0 = k < (int)gridDim.x ? p.ws_desc[k].open0 : 0;
   }
   if (last < 0) return;  // a share gave up
   const int per_tile = p.TQ * p.G;  // valid rows of a full tile
-  for (int v = blockIdx.y * 8 + warp; v < d.rows; v += gridDim.y * 8) {
+  const int v = blockIdx.y * 8 + warp;
+  if (v < d.rows) {
     const int tile = v / per_tile, r = tile * 128 + (v - tile * per_tile);
     const int tok = d.row0 + v / p.G, h = d.h0 + v % p.G;
-    if (!MIMO_ROW_OK((long long)tok * p.Hq + h, (long long)p.pb.total_q * p.Hq)) continue;
+    if (!MIMO_ROW_OK((long long)tok * p.Hq + h, (long long)p.pb.total_q * p.Hq)) return;
     const float sg = p.sinks ? p.sinks[h] * 1.4426950408889634f : -INFINITY;
     // a lane holds the statistics of one part; further parts come in rounds of 32
     const auto row_of = [&](int k) { return ((size_t)k * 2 + (k == c)) * kRows + r; };

@@ -93,22 +93,28 @@ __global__ void __launch_bounds__(kPdThreads, 2)
     int n = 0, kt = 0;  // items, tiles
     bool ok = true;
     while (ok && walk.next(p, it)) {
+      const int end = min(it.hi + 1, it.start + it.t1 * kPgKeys);
+      int k0 = it.start + it.t0 * kPgKeys;
+      // a tile's boxes and the lanes' pool rows, looked up a tile ahead of its loads
+      int boxes, row;
+      const auto look_up = [&]() {
+        PgTile tl;
+        tl.k0 = k0;
+        boxes = (min(kPdKeys, end - k0) + p.box_rows - 1) / p.box_rows;
+        row = lane < boxes ? pg_box_row(p, it, tl, lane) : 0;
+      };
+      look_up();
       const int qb = n & 1;
       if (n >= 2 && !(ok = wait_warp(&q_empty[qb], ((n >> 1) - 1) & 1, abort_flag))) break;
       const int rows = it.tokens * p.G;
       if (lane == 0) mbar_arrive_expect_tx(&q_full[qb], rows * 384);
       __syncwarp();
       if (lane < rows) {
-        const size_t row = (size_t)(it.tok0 + lane / p.G) * p.Hq + it.g * p.G + lane % p.G;
-        bulk_load(smem + kPdOffQ + qb * kPdQBytes + lane * kPdQRow, q + row * 192, 384, &q_full[qb]);
+        const size_t at = (size_t)(it.tok0 + lane / p.G) * p.Hq + it.g * p.G + lane % p.G;
+        bulk_load(smem + kPdOffQ + qb * kPdQBytes + lane * kPdQRow, q + at * 192, 384, &q_full[qb]);
       }
       ++n;
-      const int end = min(it.hi + 1, it.start + it.t1 * kPgKeys);
-      for (int k0 = it.start + it.t0 * kPgKeys; k0 < end; k0 += kPdKeys, ++kt) {
-        const int boxes = (min(kPdKeys, end - k0) + p.box_rows - 1) / p.box_rows;
-        PgTile tl;
-        tl.k0 = k0;
-        const int row = lane < boxes ? pg_box_row(p, it, tl, lane) : 0;
+      while (k0 < end) {
         const int st = kt & 1;
         if (kt >= kPdStages && !(ok = wait_warp(&empty[st], ((kt >> 1) - 1) & 1, abort_flag))) break;
         if (lane == 0) mbar_arrive_expect_tx(&full[st], boxes * p.box_rows * 640);
@@ -120,6 +126,9 @@ __global__ void __launch_bounds__(kPdThreads, 2)
 #pragma unroll
           for (int c = 0; c < 2; ++c) tma_load_3d(kb + (3 + c) * kPdBox, &tm_v, &full[st], c * 64, it.g, row);
         }
+        ++kt;
+        k0 += kPdKeys;
+        if (k0 < end) look_up();
       }
     }
     // the CTA never exits with copies in flight (after a timed-out wait the

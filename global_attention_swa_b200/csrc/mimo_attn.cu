@@ -1217,7 +1217,13 @@ mimo_status_t mimo_attn_paged_append(const mimo_attn_dims_t* dims, const void* q
     p.inv_freq[i] = (rotary_dim > 0 && i < rotary_dim / 2)
                         ? std::pow((double)rope_theta, -2.0 * i / (double)rotary_dim)
                         : 0.0;
-  mimo::paged_append_kernel<<<total_q, mimo::kPaThreads, 0, (cudaStream_t)stream>>>(p);
+  // what a thread holds of the queries at once: six vectors, as pairs that rotate and as copies
+  const int pairs = (p.Hq * (rotary_dim / 16) + mimo::kPaThreads - 1) / mimo::kPaThreads;
+  const auto kernel = pairs == 0   ? mimo::paged_append_kernel<0, 6>
+                      : pairs == 1 ? mimo::paged_append_kernel<1, 4>
+                      : pairs == 2 ? mimo::paged_append_kernel<2, 2>
+                                   : mimo::paged_append_kernel<3, 0>;
+  kernel<<<total_q, mimo::kPaThreads, 0, (cudaStream_t)stream>>>(p);
   if ((st = cuda_check(cudaGetLastError(), "paged append launch"))) return st;
   return ok();
 }

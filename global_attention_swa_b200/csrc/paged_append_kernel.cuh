@@ -8,8 +8,8 @@
 //
 // One CTA per token: the angles of a position are formed once and used by its
 // Hq + Hkv rows.  The step moves bytes and little else, so the CTA asks for the
-// token's queries first, all of them at once (16-byte vectors), and finds the
-// token's sequence, page and angles while they are on their way.
+// token's queries, keys and values first, all at once (16-byte vectors), and
+// finds the token's sequence, page and angles while they are on their way.
 #pragma once
 
 #include "paged_common.cuh"
@@ -21,8 +21,6 @@
 namespace mimo {
 
 constexpr int kPaThreads = 256;
-constexpr int kPaPairs = 3;  // vectors in flight per thread: 64 heads' worth at rotary_dim 192,
-constexpr int kPaKept = 4;   // and at 64
 
 struct PagedAppendParams {
   PagedBatch pb;
@@ -76,6 +74,10 @@ __device__ __forceinline__ int pa_kept(const PaSplit& s, int half, uint32_t w) {
   return r * 192 + 2 * half + 8 * (w - r * s.each);
 }
 
+// kPairs pairs and kKept vectors of the queries per thread are held at once, six
+// vectors in all: the 64 heads of a token at any rotary_dim that is a multiple
+// of 64 (kPairs 3 at 192, 2 at 128, 1 at 64).
+template <int kPairs, int kKept>
 __global__ void __launch_bounds__(kPaThreads, 4) paged_append_kernel(const PagedAppendParams p) {
   __shared__ float2 cs[kRaMaxHalf];
   const int t = blockIdx.x;
@@ -83,23 +85,29 @@ __global__ void __launch_bounds__(kPaThreads, 4) paged_append_kernel(const Paged
   const bool vec = half % 8 == 0;
   const __nv_bfloat16* qs = p.q + (size_t)t * p.Hq * 192;
   __nv_bfloat16* qd = p.q_out + (size_t)t * p.Hq * 192;
+  const __nv_bfloat16* ks = p.k_new + (size_t)t * p.Hkv * 192;
+  const uint4* vs = reinterpret_cast<const uint4*>(p.v_new + (size_t)t * p.Hkv * 128);
   const PaSplit turn(half / 8), keep(24 - 2 * (half / 8));
   const uint32_t qt = p.Hq * turn.each, qk = p.q == p.q_out ? 0 : p.Hq * keep.each;
+  const uint32_t kt = p.Hkv * turn.each, kk = p.Hkv * keep.each, vn = p.Hkv * 16;
   if (!MIMO_ROW_OK(t, p.pb.total_q)) return;
-  PaPair u[kPaPairs];
-  uint4 c[kPaKept];
+  PaPair u[kPairs > 0 ? kPairs : 1], ku;
+  uint4 c[kKept > 0 ? kKept : 1], kc, vc;
   if (vec) {
 #pragma unroll
-    for (int i = 0; i < kPaPairs; ++i) {
+    for (int i = 0; i < kPairs; ++i) {
       const uint32_t w = threadIdx.x + i * kPaThreads;
       if (w < qt) u[i] = pa_load(turn, half, qs, w);
     }
 #pragma unroll
-    for (int i = 0; i < kPaKept; ++i) {
+    for (int i = 0; i < kKept; ++i) {
       const uint32_t w = threadIdx.x + i * kPaThreads;
       if (w < qk) c[i] = *reinterpret_cast<const uint4*>(qs + pa_kept(keep, half, w));
     }
+    if (threadIdx.x < kt) ku = pa_load(turn, half, ks, threadIdx.x);
+    if (threadIdx.x < kk) kc = *reinterpret_cast<const uint4*>(ks + pa_kept(keep, half, threadIdx.x));
   }
+  if (threadIdx.x < vn) vc = vs[threadIdx.x];
   const int b = paged_seq_of_row(p.pb, t);  // the whole CTA takes the same branches
   if (b < 0) return;
   const PagedSeq s = paged_seq(p.pb, b);
@@ -120,28 +128,30 @@ __global__ void __launch_bounds__(kPaThreads, 4) paged_append_kernel(const Paged
     cs[threadIdx.x] = make_float2(co, sn);
   }
   __syncthreads();
-  const __nv_bfloat16* ks = p.k_new + (size_t)t * p.Hkv * 192;
   __nv_bfloat16* kd = p.k_pages + (kv ? slot : 0) * p.Hkv * 192;
+  uint4* vd = reinterpret_cast<uint4*>(p.v_pages + (kv ? slot : 0) * p.Hkv * 128);
   if (vec) {
 #pragma unroll
-    for (int i = 0; i < kPaPairs; ++i) {
+    for (int i = 0; i < kPairs; ++i) {
       const uint32_t w = threadIdx.x + i * kPaThreads;
       if (w < qt) pa_store(turn, half, qd, w, u[i], cs);
     }
 #pragma unroll
-    for (int i = 0; i < kPaKept; ++i) {
+    for (int i = 0; i < kKept; ++i) {
       const uint32_t w = threadIdx.x + i * kPaThreads;
       if (w < qk) *reinterpret_cast<uint4*>(qd + pa_kept(keep, half, w)) = c[i];
     }
+    if (kv && threadIdx.x < kt) pa_store(turn, half, kd, threadIdx.x, ku, cs);
+    if (kv && threadIdx.x < kk) *reinterpret_cast<uint4*>(kd + pa_kept(keep, half, threadIdx.x)) = kc;
     // what a CTA of this size does not hold at once
-    for (uint32_t w = threadIdx.x + kPaPairs * kPaThreads; w < qt; w += kPaThreads)
+    for (uint32_t w = threadIdx.x + kPairs * kPaThreads; w < qt; w += kPaThreads)
       pa_store(turn, half, qd, w, pa_load(turn, half, qs, w), cs);
-    for (uint32_t w = threadIdx.x + kPaKept * kPaThreads; w < qk; w += kPaThreads)
+    for (uint32_t w = threadIdx.x + kKept * kPaThreads; w < qk; w += kPaThreads)
       *reinterpret_cast<uint4*>(qd + pa_kept(keep, half, w)) = *reinterpret_cast<const uint4*>(qs + pa_kept(keep, half, w));
     if (kv) {
-      for (uint32_t w = threadIdx.x; w < p.Hkv * turn.each; w += kPaThreads)
+      for (uint32_t w = threadIdx.x + kPaThreads; w < kt; w += kPaThreads)
         pa_store(turn, half, kd, w, pa_load(turn, half, ks, w), cs);
-      for (uint32_t w = threadIdx.x; w < p.Hkv * keep.each; w += kPaThreads)
+      for (uint32_t w = threadIdx.x + kPaThreads; w < kk; w += kPaThreads)
         *reinterpret_cast<uint4*>(kd + pa_kept(keep, half, w)) = *reinterpret_cast<const uint4*>(ks + pa_kept(keep, half, w));
     }
   } else {
@@ -162,9 +172,8 @@ __global__ void __launch_bounds__(kPaThreads, 4) paged_append_kernel(const Paged
     }
   }
   if (kv) {
-    const uint4* vs = reinterpret_cast<const uint4*>(p.v_new + (size_t)t * p.Hkv * 128);
-    uint4* vd = reinterpret_cast<uint4*>(p.v_pages + slot * p.Hkv * 128);
-    for (int w = threadIdx.x; w < p.Hkv * 16; w += kPaThreads) vd[w] = vs[w];
+    if (threadIdx.x < vn) vd[threadIdx.x] = vc;
+    for (uint32_t w = threadIdx.x + kPaThreads; w < vn; w += kPaThreads) vd[w] = vs[w];
   }
 }
 

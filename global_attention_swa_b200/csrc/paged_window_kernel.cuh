@@ -197,6 +197,11 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     if (lane == 0) {
       constexpr uint32_t idesc_o = idesc_bf16_f32(128, 144, false, true);  // 128 value dims + 16 ones
       const uint32_t tO = tbase + kPwColO;
+      // One low descriptor word per operand, compile-time offsets to it: the one
+      // issuing thread is what a block's two products wait for.
+      constexpr uint32_t dhi = desc_hi_sw128(1024);
+      const uint32_t dQ0 = desc_lo_sw128(sbase + kPwOffQ, 16), dK = desc_lo_sw128(sbase + kPwOffK, 16);
+      const uint32_t dV = desc_lo_sw128(sbase + kPwOffV, kPwKBox);
       bool ok = true;
       // O = P(m) V over k keys: 16 to an MMA (P: 8 TMEM columns; V: 16 rows = 2 KB)
       const auto do_pv = [&](int m, int item, int k, bool first_of_item, bool last_of_item) {
@@ -206,9 +211,9 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         if (m >= 1 && !(ok = wait_bounded(o_empty, (m - 1) & 1, abort_flag))) return;
         tc_fence_after();
         const uint32_t tP = tbase + bm * kPwKeys;
-        const uint32_t aV = sbase + kPwOffV;
-        for (int kk = 0; kk < k / 16; ++kk)
-          umma_ts(tO, tP + kk * 8, smem_desc_sw128(aV + kk * 2048, kPwKBox, 1024), idesc_o, kk > 0 ? 1u : 0u);
+#pragma unroll
+        for (int kk = 0; kk < kPwKeys / 16; ++kk)
+          if (kk * 16 < k) umma_ts_lo(tO, tP + kk * 8, dV + ((kk * 2048) >> 4), dhi, idesc_o, kk > 0 ? 1u : 0u);
         if (last_of_item) umma_commit(v_empty);
         umma_commit(o_full);
       };
@@ -223,14 +228,12 @@ __global__ void __launch_bounds__(kPwThreads, 1)
           if (!(ok = wait_bounded(&q_full[b], (n >> 1) & 1, abort_flag))) break;
           if (blk == 0 && !(ok = wait_bounded(k_full, kp & 1, abort_flag))) break;
           tc_fence_after();
-          const uint32_t aQ = sbase + kPwOffQ + b * kPgQBytes;
-          const uint32_t aK = sbase + kPwOffK;
-          const uint32_t tS = tbase + b * kPwKeys;
+          const uint32_t dQ = dQ0 + b * (kPgQBytes >> 4), tS = tbase + b * kPwKeys;
 #pragma unroll
           for (int kk = 0; kk < 12; ++kk) {
             const uint32_t off = (kk & 3) * 32;
-            umma_ss(tS, smem_desc_sw128(aQ + (kk >> 2) * 16384 + off, 16, 1024),
-                    smem_desc_sw128(aK + (kk >> 2) * kPwKBox + off, 16, 1024), idesc_s, kk > 0 ? 1u : 0u);
+            umma_ss_lo(tS, dQ + (((kk >> 2) * 16384 + off) >> 4), dK + (((kk >> 2) * kPwKBox + off) >> 4), dhi, idesc_s,
+                       kk > 0 ? 1u : 0u);
           }
           umma_commit(&s_full[b]);
           umma_commit(&q_empty[b]);

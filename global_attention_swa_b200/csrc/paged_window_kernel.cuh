@@ -6,9 +6,8 @@
 // is kBlocks blocks.  Together they see at most window - 1 + kBlocks * TQ
 // keys; loaded in boxes of 16 from the one that holds the first, that is at
 // most kPwKeys = 160 (window 129, 16 heads to a key/value head: 2 blocks of 8
-// tokens, 159).  So there is no online softmax: maximum, exponentials and sums
-// of a row are exact, and the work of an item is one Q K^T and one P V per
-// block.  What bounds such a layer is its queries and outputs, 40 KB a block
+// tokens, 159).  So there is no online softmax, and the work of an item is one
+// Q K^T and one P V per block.  What bounds such a layer is its queries and outputs, 40 KB a block
 // against 100 KB of keys and values from L2 for an item, so the roles run as
 // a pipeline over blocks: while one block's softmax runs, the next one's
 // scores are computed and the queries of the one after are on their way.
@@ -19,7 +18,7 @@
 //   warp 14     loads V (once per item, as K) and zeroes the value rows that
 //               nothing of the item sees
 //   warps 0-7   softmax: warpgroup s takes the blocks with n & 1 == s, one row
-//               per thread, two passes over its TMEM row
+//               per thread, one pass over its TMEM row
 //   warps 8-11  epilogue: O / l -> out, lse
 //
 // The value operand carries a third 64-column block of ones and P V runs 144
@@ -312,43 +311,49 @@ __global__ void __launch_bounds__(kPwThreads, 1)
           const int hi_min = __shfl_sync(0xffffffffu, c_hi, 0), hi_max = __shfl_sync(0xffffffffu, c_hi, 31);
           const auto all_see = [&](int c) { return c >= lo_max && c + 15 <= hi_min; };
           const auto none_sees = [&](int c) { return c > hi_max || c + 15 < lo_min; };
-          // pass 1: row max over the visible columns (those at or past N are masked)
-          float mx0 = -INFINITY, mx1 = -INFINITY;
-#pragma unroll 1
-          for (int c0 = 0; c0 < N; c0 += 32) {
-            uint32_t v[32];
-            tmem_load32_sync(tS + c0, v);
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const int cq0 = c0 + 16 * q;
-              if (all_see(cq0)) {
-#pragma unroll
-                for (int e = 0; e < 16; e += 4) {
-                  mx0 = fmax3(mx0, __uint_as_float(v[16 * q + e]), __uint_as_float(v[16 * q + e + 1]));
-                  mx1 = fmax3(mx1, __uint_as_float(v[16 * q + e + 2]), __uint_as_float(v[16 * q + e + 3]));
-                }
-              } else if (!none_sees(cq0)) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                  mx0 = fmaxf(mx0, cq0 + e >= c_lo && cq0 + e <= c_hi ? __uint_as_float(v[16 * q + e]) : -INFINITY);
-              }
-            }
-          }
-          m = fmaxf(sg2, fmaxf(mx0, mx1) * p.scale_log2);
-          const float neg_m = (m == -INFINITY) ? 0.f : -m;
-          // pass 2: P = 2^(s*scale - m) (0 outside the window), bf16 over the same
+          // One pass: P = 2^(s*scale - m) (0 outside the window), bf16 over the same
           // columns (P of columns [c0, c0 + 32) lands in [c0 / 2, c0 / 2 + 16), behind
-          // the read position); the unrounded sum gives lse
+          // the read position).  The reference m is the sink's logit, or the first
+          // visible columns' maximum, and stands while no column exceeds it by more than
+          // 64: P is as exact against any reference that neither overflows nor vanishes.
+          // Else it moves up by a whole number, by which the P stored so far are scaled
+          // exactly.
           float2 l2 = make_float2(0.f, 0.f);
-          const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(neg_m, neg_m);
+          const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
 #pragma unroll 1
           for (int c0 = 0; c0 < N; c0 += 32) {
             uint32_t v[32], pk[16];
             tmem_load32_sync(tS + c0, v);
-            if (!(all_see(c0) && all_see(c0 + 16))) {
+            if (!(all_see(c0) && all_see(c0 + 16))) {  // columns at or past N are masked too
 #pragma unroll
               for (int e = 0; e < 32; ++e) v[e] = c0 + e >= c_lo && c0 + e <= c_hi ? v[e] : 0xff800000u;  // -inf
             }
+            float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              mx0 = fmax3(mx0, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+              mx1 = fmax3(mx1, __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
+            }
+            const float mx = fmaxf(mx0, mx1) * p.scale_log2;
+            const bool low = mx > m + 64.f;
+            if (__any_sync(0xffffffffu, low)) {
+              const float up = m == -INFINITY ? mx : m + ceilf(mx - m);
+              const float f = !low || m == -INFINITY ? 1.f : ex2(m - up);  // without a reference all P are 0
+              if (low) m = up;
+              if (c0 > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+                tmem_wait_st();
+#pragma unroll 1
+                for (int c = 0; c < c0 / 2; c += 16) {
+                  tmem_load16_sync(tS + c, pk);
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) pk[e] = pack_bf16(bf16_lo(pk[e]) * f, bf16_hi(pk[e]) * f);
+                  tmem_st16(tS + c, pk);
+                }
+              }
+              l2 = make_float2(l2.x * f, l2.y * f);
+            }
+            const float neg_m = (m == -INFINITY) ? 0.f : -m;
+            const float2 nm2 = make_float2(neg_m, neg_m);
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               const float2 y = fma2(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), sc2, nm2);

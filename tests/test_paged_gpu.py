@@ -161,12 +161,15 @@ def test_extreme_sinks(sink, n):
     check(*attend(x), oracle_of(x))
 
 
+@pytest.mark.parametrize("sink", [None, -40.0])
+@pytest.mark.parametrize("window", [0, 129])
 @pytest.mark.parametrize("n", [1, 6, 40])
-def test_large_scores(n):
-    """Scores of several hundred, both signs: no weight overflows, none is lost."""
-    x = build([700], [n], 0, 16, 16, 1, seed=8)
+def test_large_scores(n, window, sink):
+    """Scores of several hundred, both signs, rising along the row: no weight overflows,
+    none is lost, and a reference that was taken early is moved."""
+    x = build([700], [n], window, 16, 16, 1, seed=8)
     x["q"] *= 16
-    x["sinks"] = None
+    x["sinks"] = None if sink is None else torch.full((16,), sink)
     out, lse = attend(x, out_dtype=torch.float32)
     want, want_lse, mass = oracle_of(x)
     # the scores are 16 times those of the module's bound, so is their error: 4.2e-3

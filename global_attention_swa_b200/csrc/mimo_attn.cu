@@ -888,6 +888,8 @@ namespace {
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+constexpr long kMaxPositions = (1L << 31) - 1024;
+
 // The sizes and tables every call over a paged cache takes.
 mimo_status_t check_paged(const int32_t* block_table, const int32_t* cu_seqlens_q, const int32_t* seqlens,
                           int num_seqs, int total_q, int max_seqlen_q, int num_pages, int page_size,
@@ -897,8 +899,9 @@ mimo_status_t check_paged(const int32_t* block_table, const int32_t* cu_seqlens_
   if (num_pages <= 0 || page_size <= 0 || max_pages <= 0)
     return fail(MIMO_ERR_INVALID_ARG, "num_pages, page_size and max_pages must be positive");
   if (page_size % 16) return fail(MIMO_ERR_UNSUPPORTED, "page_size must be a multiple of 16 (got %d)", page_size);
-  if ((long)num_pages * page_size > 0x7fffffffL || (long)max_pages * page_size > 0x7fffffffL)
-    return fail(MIMO_ERR_UNSUPPORTED, "num_pages * page_size and max_pages * page_size must fit in int32");
+  // positions and pool rows are int32, and kernels step a tile or two past the last
+  if ((long)num_pages * page_size > kMaxPositions || (long)max_pages * page_size > kMaxPositions)
+    return fail(MIMO_ERR_UNSUPPORTED, "num_pages * page_size and max_pages * page_size must be at most 2^31 - 1024");
   if (max_seqlen_q > total_q)
     return fail(MIMO_ERR_INVALID_ARG, "max_seqlen_q (%d) > total_q (%d)", max_seqlen_q, total_q);
   if (!block_table || !cu_seqlens_q || !seqlens)
@@ -1029,19 +1032,24 @@ mimo_status_t check_page_table(const int32_t* page_refs, int num_pages, const in
 
 // One cluster of CTAs over `elements` array elements: enough that each thread
 // passes over a few.
-template <typename Params>  // each kernel has its own: `done` is the kernel's
+template <typename Params>  // each kernel has its own: `most` is the kernel's
 mimo_status_t launch_cluster(void (*kernel)(Params), const Params& p, long elements, void* stream, const char* what) {
-  static std::atomic<bool> done[64];  // per device: clusters past the portable size are allowed
+  static std::atomic<int> most[64];  // per device: the largest cluster this kernel can have, 0 = not asked yet
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return fail(MIMO_ERR_CUDA, "cudaGetDevice failed");
-  if (!done[dev].load(std::memory_order_acquire)) {
-    const mimo_status_t st =
-        cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1), what);
+  int limit = most[dev].load(std::memory_order_acquire);
+  if (limit == 0) {
+    mimo_status_t st = cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1), what);
     if (st) return st;
-    done[dev].store(true, std::memory_order_release);
+    cudaLaunchConfig_t ask = {};
+    ask.gridDim = dim3(mimo::kPtMaxCtas);
+    ask.blockDim = dim3(mimo::kPtThreads);
+    if ((st = cuda_check(cudaOccupancyMaxPotentialClusterSize(&limit, kernel, &ask), what))) return st;
+    limit = std::max(1, std::min(limit, mimo::kPtMaxCtas));
+    most[dev].store(limit, std::memory_order_release);
   }
   int ctas = 1;
-  while (ctas < mimo::kPtMaxCtas && elements > (long)ctas * 2 * mimo::kPtThreads) ctas *= 2;
+  while (2 * ctas <= limit && elements > (long)ctas * 2 * mimo::kPtThreads) ctas *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(mimo::kPtThreads);
@@ -1242,8 +1250,8 @@ mimo_status_t mimo_attn_page_hold(const int32_t* page_refs, int num_pages, const
                                       block_table_out);
   if (st) return st;
   if (page_size <= 0) return fail(MIMO_ERR_INVALID_ARG, "page_size must be positive (got %d)", page_size);
-  if ((long)max_pages * page_size > 0x7fffffffL)
-    return fail(MIMO_ERR_UNSUPPORTED, "max_pages * page_size must fit in int32");
+  if ((long)max_pages * page_size > kMaxPositions)
+    return fail(MIMO_ERR_UNSUPPORTED, "max_pages * page_size must be at most 2^31 - 1024");
   if ((num_seqs > 0 && (!seqlens || !moves)) || !info)
     return fail(MIMO_ERR_INVALID_ARG, "seqlens, moves and info must be non-NULL");
   if (!aligned4(seqlens) || !aligned4(first) || !aligned4(write_from) || !aligned4(moves) || !aligned4(info))

@@ -52,6 +52,7 @@ class PagedCache:
         self.info = torch.zeros(2, **ints)
         self._kept = torch.zeros(num_seqs, **ints)  # first position whose page was never released
         self.page_size, self.window, self.rollback = page_size, window, rollback
+        self.capacity = max_pages * page_size
 
     def _first(self, lens, more):
         """First position that queries from lens - more on see; never one already released."""
@@ -69,12 +70,14 @@ class PagedCache:
         """Pages for new_tokens [num_seqs] int32 more positions of each sequence, and its
         length advanced over them.  A page that a fork shares and that will be written
         is replaced by a copy, in every layer.  If the pool does not have the pages,
-        nothing changes and ``info[0]`` says how many were missing.  Returns ``info``."""
+        nothing changes and ``info[0]`` says how many were missing; a sequence that
+        would pass max_pages pages stays as it is and is recorded as an invalid
+        argument in the device status.  Returns ``info``."""
         lens = self.seqlens + new_tokens
         first = self._first(self.seqlens, self.rollback)
         moves = self._hold(lens, first, self.seqlens)
         mimo.mimo_attn_page_copy(self.k_pages, self.v_pages, moves)
-        done = self.info[0] == 0
+        done = (self.info[0] == 0) & (lens >= 0) & (lens <= self.capacity)
         self.seqlens.copy_(torch.where(done, lens, self.seqlens))
         if first is not None:
             self._kept.copy_(torch.where(done, first, self._kept))
@@ -100,19 +103,21 @@ class PagedCache:
         last ``extend`` less ``rollback``, or to 0."""
         lens = torch.minimum(lens, self.seqlens)
         self._hold(lens, self._first(lens, 0), None)
-        self.seqlens.copy_(lens)
-        self._kept.mul_(lens > 0)
+        self.seqlens.copy_(torch.where(lens >= 0, lens, self.seqlens))  # a negative one was recorded
+        self._kept.mul_(lens != 0)
         return self.info
 
     def fork(self, parent):
         """Slot i goes on as slot parent[i] [num_seqs] int32 was, sharing its pages; a
-        negative parent leaves the slot empty."""
+        negative parent leaves the slot empty (so does one that is no slot, and is
+        recorded as an invalid argument in the device status)."""
         mimo.mimo_attn_page_fork(self.page_refs, self.block_table, parent, refs_out=self.page_refs,
                                  table_out=self._spare_table)
         self.block_table.copy_(self._spare_table)
-        source = parent.clamp(min=0).long()
+        slots = self.seqlens.numel()
+        source, real = parent.clamp(0, slots - 1).long(), (parent >= 0) & (parent < slots)
         for t in (self.seqlens, self._kept):
-            t.copy_(t[source] * (parent >= 0))
+            t.copy_(t[source] * real)
 
     def compact(self, max_moves):
         """Move used pages from the end of the pools to free places at their front, at most

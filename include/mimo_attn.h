@@ -335,7 +335,7 @@ mimo_status_t mimo_attn_decode_noalloc(const mimo_attn_dims_t* dims, const void*
  *
  * page_size is a multiple of 16 for the calls that read or write keys and
  * values (else MIMO_ERR_UNSUPPORTED); num_pages * page_size and max_pages *
- * page_size fit in int32.  Packed rows from cu[num_seqs] on (up to total_q)
+ * page_size are at most 2^31 - 1024.  Packed rows from cu[num_seqs] on (up to total_q)
  * belong to no sequence: their outputs are left as they were.
  *
  * A sequence with n_b < 0, rows outside [0, total_q), n_b > max_seqlen_q, n_b >
@@ -487,7 +487,8 @@ mimo_status_t mimo_attn_device_status(void* stream);
  * ordered on `stream`: kernels launched on it afterwards see the new value.
  * A diagnostic hook for testing the failure path without a failing GPU.
  * With MIMO_ERR_TIMEOUT pre-loaded, every kernel that has bounded waits
- * (prefill, decode, FP8 decode, the decode combine, the tcgen05 backward)
+ * (prefill, decode, FP8 decode, the decode combine, the tcgen05 backward, the
+ * paged attention and its combine)
  * returns at entry, as it does after a real timed-out wait elsewhere, and
  * writes none of its outputs.  mimo_attn_device_status() then reports the
  * code and clears it.  Codes outside 0..5 return MIMO_ERR_INVALID_ARG.

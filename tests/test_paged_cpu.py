@@ -31,7 +31,7 @@ def _attend(hq=64, hkv=4, dqk=192, q=FAKE, k=FAKE, v=FAKE, table=FAKE, cu=FAKE, 
     (dict(window=-1), INVALID), (dict(seqs=-1), INVALID), (dict(total=-1), INVALID), (dict(most=-1), INVALID),
     (dict(most=9), INVALID), (dict(pages=0), INVALID), (dict(ps=0), INVALID), (dict(width=0), INVALID),
     (dict(ps=8), UNSUPPORTED), (dict(ps=40), UNSUPPORTED), (dict(pages=1 << 26), UNSUPPORTED),
-    (dict(width=1 << 26), UNSUPPORTED), (dict(q=0), INVALID), (dict(k=0), INVALID), (dict(v=0), INVALID),
+    (dict(width=1 << 26), UNSUPPORTED), (dict(pages=(1 << 25) - 1), UNSUPPORTED), (dict(q=0), INVALID), (dict(k=0), INVALID), (dict(v=0), INVALID),
     (dict(out=0), INVALID), (dict(table=0), INVALID), (dict(cu=0), INVALID), (dict(lens=0), INVALID),
     (dict(q=FAKE + 2), INVALID), (dict(k=FAKE + 8), INVALID), (dict(out=FAKE + 4), INVALID),
     (dict(lse=FAKE + 2), INVALID), (dict(sinks=FAKE + 1), INVALID), (dict(table=FAKE + 2), INVALID),

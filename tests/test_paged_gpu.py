@@ -653,6 +653,56 @@ def test_a_serving_run(window, ps):
     assert torch.equal(cache.block_table, before[0]) and torch.equal(cache.page_refs, before[1])
 
 
+def test_the_cache_keeps_its_sequences_through_bad_requests():
+    """Past the table's width, a negative length, a parent that is no slot: recorded, the
+    rest goes on, nothing is lost."""
+    cache = PagedCache(1, 32, 16, 3, 4, 1)
+    cache.extend(ints([20, 30, 5]).cuda())
+    mimo.mimo_attn_device_status()
+    for call, lens in ((lambda: cache.extend(ints([1, 100, 1]).cuda()), [21, 30, 6]),
+                       (lambda: cache.truncate(ints([21, -4, 2]).cuda()), [21, 30, 2]),
+                       (lambda: cache.fork(ints([1, 7, 0]).cuda()), [30, 0, 21])):
+        call()
+        with pytest.raises(mimo.MimoAttnError) as e:
+            mimo.mimo_attn_device_status()
+        assert e.value.status == mimo.MIMO_ERR_INVALID_ARG
+        assert cache.seqlens.tolist() == lens
+        held = [sum(x >= 0 for x in row) for row in cache.block_table.tolist()]
+        assert held == [-(-n // 16) for n in lens] and int(cache.page_refs.sum()) == sum(held)
+
+
+@pytest.mark.parametrize("n,window", [(1, 0), (1, 129), (5, 0), (40, 0), (40, 129)])
+def test_after_a_recorded_timeout_nothing_is_written(n, window):
+    x = build([300, 60], [n, n], window, 16, 16, 1, seed=2)
+    dev = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in x.items()}
+    out = torch.full((2 * n, 16, 128), 7.0, device="cuda")
+    lse = torch.full((16, 2 * n), 7.0, device="cuda")
+    call = lambda: mimo.mimo_attn_paged_attention(dev["q"], dev["kp"], dev["vp"], dev["table"], dev["cu"], dev["lens"],  # noqa: E731
+                                                  n, window, dev["sinks"], out=out, lse=lse)
+    mimo.mimo_attn_set_device_status(mimo.MIMO_ERR_TIMEOUT)
+    call()
+    with pytest.raises(mimo.MimoAttnError) as e:
+        mimo.mimo_attn_device_status()
+    assert e.value.status == mimo.MIMO_ERR_TIMEOUT
+    assert torch.all(out == 7) and torch.all(lse == 7)
+    call()
+    mimo.mimo_attn_device_status()
+    check(out, lse, oracle_of(x))
+
+
+def test_many_sequences():
+    """More sequences than a CTA has threads, most of them without new tokens."""
+    r = random.Random(1)
+    lens = [r.randint(1, 40) for _ in range(900)]
+    for n in (1, 3, 20):
+        for window in (0, 9):
+            news = [min(L, n) if r.random() < 0.1 else 0 for L in lens]
+            news[-1] = min(lens[-1], n)
+            x = build(lens, news, window, 16, 4, 1, seed=n)
+            x["most"] = n
+            check(*attend(x), oracle_of(x))
+
+
 def test_a_step_captured_in_a_graph_and_replayed():
     """extend, append, attention and truncate of a decode step, captured once; each replay
     against an eager twin of the cache."""

@@ -929,7 +929,7 @@ mimo::PagedBatch paged_batch(const int32_t* block_table, const int32_t* cu_seqle
 
 // Which kernel a call over a paged cache takes, by the most new tokens a
 // sequence brings and the G query heads of a key/value head.
-//   decode  at most 16 rows to a key/value head: warp-level MMAs, two CTAs to an SM
+//   decode  one token, G <= 16: warp-level MMAs, two CTAs to an SM
 //   window  all keys of one or two blocks of 128 / G tokens fit a score tile
 //   tile    one tile of 128 / G tokens, or two that share their key tiles
 struct PagedVariant {
@@ -953,9 +953,9 @@ PagedVariant paged_variant(const mimo_attn_dims_t* dims, int max_seqlen_q, int w
   v.kind = PagedVariant::tile;
   v.ctas = sms;
   const auto span = [&](int tiles) { return window - 1L + (long)tiles * v.TQ + mimo::kPwBoxRows - 1; };
-  if (G <= mimo::kPdRows && max_seqlen_q <= mimo::kPdRows / G) {
+  if (max_seqlen_q == 1 && G <= mimo::kPdRows) {
     v.kind = PagedVariant::decode;
-    v.TQ = mimo::kPdRows / G;
+    v.TQ = 1;
     v.tiles = 1;
     v.ctas = 2 * sms;
   } else if (window > 0 && span(1) <= mimo::kPwKeys) {
@@ -1107,6 +1107,9 @@ mimo_status_t mimo_attn_paged_attention(const mimo_attn_dims_t* dims, const void
   mimo::PagedAttnParams p;
   p.pb = paged_batch(block_table, cu_seqlens_q, seqlens, num_seqs, total_q, max_seqlen_q, num_pages, page_size,
                      max_pages);
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k_pages);
+  p.v = static_cast<const __nv_bfloat16*>(v_pages);
   p.sinks = sinks;
   p.out = out;
   p.lse = lse;
@@ -1157,8 +1160,7 @@ mimo_status_t mimo_attn_paged_attention(const mimo_attn_dims_t* dims, const void
   const int ctas = v.split ? v.ctas : (int)std::min<long>(v.ctas, items);
   const cudaStream_t cs = (cudaStream_t)stream;
   if (v.kind == PagedVariant::decode)
-    mimo::paged_decode_kernel<<<ctas, mimo::kPdThreads, mimo::kPdSmemBytes, cs>>>(
-        tk, tv, static_cast<const __nv_bfloat16*>(q), p);
+    mimo::paged_decode_kernel<<<ctas, mimo::kPdThreads, mimo::kPdSmemBytes, cs>>>(tk, tv, p);
   else if (v.kind == PagedVariant::window && v.tiles == 1)
     mimo::paged_window_kernel<1><<<ctas, mimo::kPwThreads, mimo::kPwSmemBytes, cs>>>(tq, tk, tv, p);
   else if (v.kind == PagedVariant::window)

@@ -21,9 +21,9 @@
 //
 //   warp 8      loads Q and K (TMA), allocates TMEM
 //   warp 9      issues the MMAs (one thread): S = Q K^T (SS), O += P V (TS, P from TMEM)
-//   warp 10     loads V (TMA) and zeroes the value rows of a key tile that the
-//               item does not see (they may hold anything, and 0 * NaN would
-//               reach the sum); warp 11 completes the warpgroup
+//   warp 10     loads V (TMA) and keeps values out of the sum that must not reach
+//               it (pg_zero_unseen, pg_look)
+//   warp 11     works out the items of this CTA's share, ahead of the others
 //   warps 0-3   softmax and epilogue of tile 0 (one row per thread)
 //   warps 4-7   softmax and epilogue of tile 1
 //
@@ -60,8 +60,8 @@ struct PgLayout {
   static constexpr int kOffK = kTiles * kPgQBytes;
   static constexpr int kOffV = kOffK + kPgKStages * kPgKBytes;
   static constexpr int kOffBar = kOffV + kVStages * kPgVBytes;
-  static constexpr int kOffItems = kOffBar + 384;             // barriers and plan before it
-  static constexpr int kSmemBytes = kOffItems + 8 * 128 + 1024;  // a walk and item per softmax warp; alignment slack
+  static constexpr int kOffItems = kOffBar + 512;                      // barriers and plan before it
+  static constexpr int kSmemBytes = kOffItems + 512 + 1024;  // the queue of items; alignment slack
 };
 
 // Partial results in the workspace: one descriptor per CTA, then for each CTA
@@ -78,6 +78,9 @@ struct PgDesc {
 
 struct PagedAttnParams {
   PagedBatch pb;
+  const __nv_bfloat16* q;  // [total_q, Hq, 192]
+  const __nv_bfloat16* k;  // [num_pages, page_size, Hkv, 192]
+  const __nv_bfloat16* v;  // [num_pages, page_size, Hkv, 128]
   const float* sinks;      // [Hq] or null
   void* out;               // [total_q, Hq, 128]
   float* lse;              // [Hq, total_q] or null
@@ -161,11 +164,16 @@ struct PgItem {
   int p0;           // that token's position
   int tokens;       // valid tokens, 1 .. kTiles * TQ
   int lo, hi;       // keys that some row sees: [lo, hi]
+  int early;        // of those, [lo, early) and (p0, hi] are hidden from some rows
   int start;        // first key of tile 0: lo rounded down to a box
   int n_kt;         // key tiles
   int t0, t1;       // the tiles of this share
   int turn;         // the order of their passage: from t0 + turn on, then from t0
+  int n_last;       // keys that the products take of the last tile, a multiple of 16
+  int e0, e1;       // tiles below e0 and from e1 on are edges (PgTile::edge)
   __device__ __forceinline__ int count() const { return t1 - t0; }
+  __device__ __forceinline__ int width(int t) const { return t == n_kt - 1 ? n_last : kPgKeys; }
+  __device__ __forceinline__ bool edge(int t) const { return t < e0 || t >= e1; }
   // The tile that passes j-th.
   __device__ __forceinline__ int tile(int j) const {
     const int t = t0 + turn + j;
@@ -194,7 +202,6 @@ struct PgWalk {
   __device__ __forceinline__ PgWalk(const PagedAttnParams& p, const PgPlace* plan) : at(plan[0]), end(plan[1]), first(true), passed(0) {
     seq(p);
   }
-  __device__ __forceinline__ PgWalk() {}
   // The next item with work in this share; false at its end.
   __device__ __forceinline__ bool next(const PagedAttnParams& p, PgItem& it) {
     while (true) {
@@ -222,8 +229,13 @@ struct PgWalk {
       it.tokens = min(D, s.n - at.i * D);
       it.hi = it.p0 + it.tokens - 1;
       it.lo = p.window > 0 ? max(0, it.p0 - p.window + 1) : 0;
+      it.early = p.window > 0 ? max(it.lo, it.hi - p.window + 1) : it.lo;
       it.start = it.lo / p.box_rows * p.box_rows;
       it.n_kt = (it.hi - it.start) / kPgKeys + 1;
+      const int left = it.hi + 1 - (it.start + (it.n_kt - 1) * kPgKeys);
+      it.n_last = min(kPgKeys, (left + 15) & ~15);
+      it.e0 = (max(it.early, it.lo) - it.start + kPgKeys - 1) / kPgKeys;
+      it.e1 = it.hi > it.p0 ? (it.p0 + 1 - it.start) / kPgKeys : left < it.n_last ? it.n_kt - 1 : it.n_kt;
       it.t0 = at.t;
       it.t1 = last ? min(end.t, it.n_kt) : it.n_kt;
       if (it.t0 < it.t1) {
@@ -240,20 +252,122 @@ struct PgWalk {
   }
 };
 
-// Key tile t of an item: its first key, how many the products take (a multiple
-// of 16), and the rows [0, zlo) and [zhi, n) that nothing of the item sees.
+// A key tile of an item: its first key, how many the products take (a multiple
+// of 16), and rows of it: [0, zlo) and [zhi, n) are seen by nothing, [lo, lo_end)
+// and [hi, hi_end) by some rows only.
 struct PgTile {
-  int k0, n, zlo, zhi;
-  __device__ __forceinline__ bool edge() const { return zlo > 0 || zhi < n; }
+  int k0, n, zlo, zhi, lo, lo_end, hi, hi_end;
+  // Its values are looked through before the product.
+  __device__ __forceinline__ bool edge() const { return zlo > 0 || zhi < n || lo_end > lo || hi_end > hi; }
 };
-__device__ __forceinline__ PgTile pg_tile(const PgItem& it, int t) {
+__device__ __forceinline__ PgTile pg_keys(const PgItem& it, int k0, int most) {
   PgTile r;
-  r.k0 = it.start + t * kPgKeys;
-  const int left = it.hi + 1 - r.k0;
-  r.n = min(kPgKeys, (left + 15) & ~15);
-  r.zlo = max(0, it.lo - r.k0);
+  r.k0 = k0;
+  const int left = it.hi + 1 - k0;
+  r.n = min(most, (left + 15) & ~15);
+  r.zlo = max(0, it.lo - k0);
   r.zhi = min(r.n, left);
+  r.lo = r.zlo;
+  r.lo_end = min(r.zhi, it.early - k0);
+  r.hi = max(0, it.p0 + 1 - k0);
+  r.hi_end = r.zhi;
   return r;
+}
+__device__ __forceinline__ PgTile pg_tile(const PgItem& it, int t) { return pg_keys(it, it.start + t * kPgKeys, kPgKeys); }
+
+// 0 * v is NaN where v is not finite, so a value row must not enter the product
+// of rows that do not see its key.  Rows that nothing sees are zeroed in shared
+// memory.  Rows that some rows of the item see are looked over, and where one
+// holds a value that is not finite it is zeroed too, and the epilogue adds it to
+// the rows that see it (pg_add_hidden).  All by one warp; vb: shared address of
+// [rows][64 columns] boxes `box` bytes apart.
+__device__ __forceinline__ bool bf16x2_not_finite(uint32_t u) {
+  return (u & 0x7F80u) == 0x7F80u || (u & 0x7F800000u) == 0x7F800000u;
+}
+__device__ __forceinline__ bool not_finite(const uint4& u) {
+  return bf16x2_not_finite(u.x) || bf16x2_not_finite(u.y) || bf16x2_not_finite(u.z) || bf16x2_not_finite(u.w);
+}
+__device__ __forceinline__ uint4 lds_v4(uint32_t addr) {
+  uint4 u;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(addr) : "memory");
+  return u;
+}
+__device__ __forceinline__ void sts_zero(uint32_t addr) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0) : "memory");
+}
+// Shared address of vector w of a list of value rows, 16 vectors a row (8 in each
+// box): [0, na) of the list from row a on, the rest from row b on.
+__device__ __forceinline__ uint32_t pg_vec(uint32_t vb, int box, int w, int a, int na, int b) {
+  const int i = w >> 4;
+  return vb + ((w >> 3) & 1) * box + (i < na ? a + i : b + i - na) * 128 + (w & 7) * 16;
+}
+// Zeroes the rows that nothing sees.
+__device__ __forceinline__ void pg_zero_unseen(const PgTile& tl, uint32_t vb, int box) {
+  for (int w = threadIdx.x & 31; w < (tl.zlo + tl.n - tl.zhi) * 16; w += 32)
+    sts_zero(pg_vec(vb, box, w, 0, tl.zlo, tl.zhi));
+}
+// Whether the rows that only some rows of the item see hold a value that is not finite.
+__device__ __forceinline__ bool pg_look(const PgTile& tl, uint32_t vb, int box) {
+  const int lane = threadIdx.x & 31;
+  const int na = max(0, tl.lo_end - tl.lo), rows = na + max(0, tl.hi_end - tl.hi);
+  bool any = false;
+#pragma unroll 1
+  for (int w0 = 0; w0 < rows * 16; w0 += 256) {
+    uint4 u[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {  // past the end: the first vector again
+      const int w = w0 + 32 * i + lane;
+      u[i] = lds_v4(pg_vec(vb, box, w < rows * 16 ? w : 0, tl.lo, na, tl.hi));
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) any |= not_finite(u[i]);
+  }
+  return __any_sync(0xffffffffu, any);
+}
+// Zeroes those of them that do.
+__device__ __forceinline__ void pg_take_out(const PgTile& tl, uint32_t vb, int box) {
+  const int lane = threadIdx.x & 31;
+  const int na = max(0, tl.lo_end - tl.lo), rows = na + max(0, tl.hi_end - tl.hi);
+#pragma unroll 1
+  for (int w0 = 0; w0 < rows * 16; w0 += 32) {  // two rows at a time
+    const int w = w0 + lane;
+    const uint32_t at = pg_vec(vb, box, w, tl.lo, na, tl.hi);
+    const bool bad = w < rows * 16 && not_finite(lds_v4(at));
+    if (__ballot_sync(0xffffffffu, bad) >> (lane & 16) & 0xFFFFu) sts_zero(at);
+  }
+}
+
+// The items of a CTA's share, worked out by one thread and read by every role: a
+// ring of kPgItems in shared memory.  (Walking the list in each role instead cost
+// a copy of that code per role, more instructions than their cache holds beside
+// the loops, and its latency in each.)
+constexpr int kPgItems = 4;
+struct PgQueue {
+  PgItem it[kPgItems];
+  int more[kPgItems];   // 0: past the last item
+  int dirty[kPgItems];  // pg_look found something
+};
+template <int kTiles>
+__device__ __forceinline__ void pg_schedule(const PagedAttnParams& p, const PgPlace* plan, PgQueue& q, uint64_t* full,
+                                            uint64_t* empty, volatile int* abort) {
+  PgWalk<kTiles> walk(p, plan);
+  bool more = true;
+  for (int n = 0; more; ++n) {
+    const int s = n % kPgItems;
+    if (n >= kPgItems && !wait_bounded(&empty[s], (n / kPgItems - 1) & 1, abort)) return;
+    PgItem it;
+    more = walk.next(p, it);
+    q.it[s] = it;
+    q.more[s] = more;
+    q.dirty[s] = 0;
+    mbar_arrive(&full[s]);
+  }
+}
+// Item n is there to read; false past the last one, or after a timed-out wait.
+// Each reader arrives once on empty[n % kPgItems] when it is done with it.
+__device__ __forceinline__ bool pg_item(const PgQueue& q, uint64_t* full, int n, volatile int* abort) {
+  const int s = n % kPgItems;
+  return wait_bounded(&full[s], (n / kPgItems) & 1, abort) && *const_cast<const volatile int*>(&q.more[s]);
 }
 
 // This CTA's share.  All threads call it; plan (shared) holds the first place
@@ -327,10 +441,52 @@ __device__ __forceinline__ int pg_box_row(const PagedAttnParams& p, const PgItem
   return e < 0 ? p.pb.num_pages * p.pb.page_size : e * p.pb.page_size + (pos - page * p.pb.page_size);
 }
 
+// What was taken out of the product: adds P v to `kN` columns (from column c0 on)
+// of the row (packed row tok, head h, position pos, reference m) for the keys in
+// [k_begin, k_end) that it sees, some rows of its item do not, and whose values
+// are not all finite.
+template <int kN>
+__device__ __noinline__ void pg_add_hidden(const PagedAttnParams& p, const PgItem& it, int k_begin, int k_end, int tok,
+                                           int h, int pos, float m, int c0, float (&o)[kN]) {
+  const int see = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+#pragma unroll 1
+  for (int j = max(it.lo, k_begin); j < min(it.hi + 1, k_end); ++j) {
+    if (j >= it.early && j <= it.p0) {  // every row sees these
+      j = it.p0;
+      continue;
+    }
+    if (j < see || j > pos) continue;
+    const int e = p.pb.table[(size_t)it.b * p.pb.max_pages + j / p.pb.page_size];
+    if (e < 0 || e >= p.pb.num_pages) continue;
+    const size_t row = ((size_t)e * p.pb.page_size + j % p.pb.page_size) * p.Hkv + it.g;
+    const uint4* v = reinterpret_cast<const uint4*>(p.v + row * 128);
+    bool bad = false;
+#pragma unroll 1
+    for (int i = 0; i < 16 && !bad; ++i) bad = not_finite(v[i]);
+    if (!bad) continue;
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(p.q + ((size_t)tok * p.Hq + h) * 192);
+    const uint32_t* k = reinterpret_cast<const uint32_t*>(p.k + row * 192);
+    float s = 0.f;
+#pragma unroll 1
+    for (int i = 0; i < 96; ++i) s += bf16_lo(q[i]) * bf16_lo(k[i]) + bf16_hi(q[i]) * bf16_hi(k[i]);
+    const float pe = bf16_lo(pack_bf16(ex2(s * p.scale_log2 - m), 0.f));  // as the product would have it
+#pragma unroll
+    for (int i = 0; i < kN / 8; ++i) {
+      const uint4 u = v[c0 / 8 + i];
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        o[8 * i + 2 * x] += pe * bf16_lo(w[x]);
+        o[8 * i + 2 * x + 1] += pe * bf16_hi(w[x]);
+      }
+    }
+  }
+}
+
 template <int kTiles>
 __global__ void __launch_bounds__(kPgThreads, 1)
     paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                           const __grid_constant__ CUtensorMap tm_v, const PagedAttnParams p) {
+                           const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedAttnParams p) {
   using Lay = PgLayout<kTiles>;
   constexpr int kVStages = Lay::kVStages;
   extern __shared__ __align__(1024) uint8_t pgsmem_raw[];
@@ -352,8 +508,13 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 22);
   volatile int* never_flag = reinterpret_cast<volatile int*>(bars + 23);  // never raised
   int* armed = reinterpret_cast<int*>(bars + 24);  // [4]: phases armed on Q, K, V; the MMA thread had work
-  PgPlace* plan = reinterpret_cast<PgPlace*>(bars + 26);             // [2]
-  long long* warp_sum = reinterpret_cast<long long*>(bars + 32);     // [12]
+  PgPlace* plan = reinterpret_cast<PgPlace*>(bars + 26);          // [2]
+  uint64_t* i_full = bars + 30;                                      // [kPgItems]
+  uint64_t* i_empty = bars + 34;                                     // [kPgItems]
+  long long* warp_sum = reinterpret_cast<long long*>(bars + 40);     // [12]
+  static_assert(sizeof(PgQueue) <= 512, "the queue's place");
+  PgQueue& queue = *reinterpret_cast<PgQueue*>(smem + Lay::kOffItems);
+  constexpr int kReaders = 3 + 4 * kTiles;  // warps 8, 9, 10 and the softmax warps
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -375,6 +536,10 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         mbar_init(&p_full[i], 128);
         mbar_init(&o_full[i], 1);
         mbar_init(&o_empty[i], 128);
+      }
+      for (int i = 0; i < kPgItems; ++i) {
+        mbar_init(&i_full[i], 1);
+        mbar_init(&i_empty[i], kReaders);
       }
       mbar_init(mma_drain, 1);
       *never_flag = 0;
@@ -404,11 +569,12 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   if (warp == 8) {
     // ------------------------------------------------------------ Q and K
     if (work) {
-      PgWalk<kTiles> walk(p, plan);
-      PgItem it;
       int n = 0, kt = 0;  // items and key tiles loaded
       bool ok = true;
-      while (ok && walk.next(p, it)) {
+      while (ok && pg_item(queue, i_full, n, abort_flag)) {
+        const PgItem it = queue.it[n % kPgItems];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&i_empty[n % kPgItems]);
         if (n > 0 && !(ok = wait_warp(q_empty, (n - 1) & 1, abort_flag))) break;
         const bool has1 = kTiles == 2 && it.tokens > p.TQ;
         if (lane == 0) {
@@ -446,11 +612,10 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   } else if (warp == 10) {
     // ------------------------------------------------------------ V
     if (work) {
-      PgWalk<kTiles> walk(p, plan);
-      PgItem it;
       int kt = 0;
       bool ok = true;
-      while (ok && walk.next(p, it)) {
+      for (int n = 0; ok && pg_item(queue, i_full, n, abort_flag); ++n) {
+        const PgItem it = queue.it[n % kPgItems];
         for (int j = 0; j < it.count(); ++j, ++kt) {
           const PgTile tl = pg_tile(it, it.tile(j));
           const int boxes = (tl.n + p.box_rows - 1) / p.box_rows;
@@ -467,21 +632,25 @@ __global__ void __launch_bounds__(kPgThreads, 1)
 #pragma unroll
             for (int c = 0; c < 2; ++c) tma_load_3d(dst + c * 16384, &tm_v, &v_full[vs], c * 64, it.g, row);
           }
-          if (tl.edge()) {  // at most two tiles of an item
+          if (it.edge(it.tile(j))) {
             if (!(ok = wait_warp(&v_full[vs], (kt / kVStages) & 1, abort_flag))) break;
-            uint8_t* vb = smem + Lay::kOffV + vs * kPgVBytes;
-            const int rows = tl.zlo + tl.n - tl.zhi;
-            for (int w = lane; w < rows * 16; w += 32) {  // 16 vectors a row: 8 in each 64-column box
-              const int i = w >> 4, r = i < tl.zlo ? i : tl.zhi + (i - tl.zlo);
-              *reinterpret_cast<uint4*>(vb + ((w >> 3) & 1) * 16384 + r * 128 + (w & 7) * 16) = make_uint4(0, 0, 0, 0);
+            const uint32_t vb = sbase + Lay::kOffV + vs * kPgVBytes;
+            pg_zero_unseen(tl, vb, 16384);
+            if (pg_look(tl, vb, 16384)) {
+              pg_take_out(tl, vb, 16384);
+              if (lane == 0) queue.dirty[n % kPgItems] = 1;
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&v_ready[vs]);
           }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&i_empty[n % kPgItems]);
       }
     }
+  } else if (warp == 11) {
+    if (lane == 0 && work) pg_schedule<kTiles>(p, plan, queue, i_full, i_empty, abort_flag);
   } else if (warp == 9) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0 && work) {
@@ -510,8 +679,6 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         for (int kk = 0; kk < 8; ++kk)
           if (kk * 16 < n) umma_ts_lo(tO, tP + kk * 8, dV + ((kk * 2048) >> 4), dhi, idesc_o, (acc || kk > 0) ? 1u : 0u);
       };
-      PgWalk<kTiles> walk(p, plan);
-      PgItem it;
       int n = 0, n1 = 0;   // items, those with a second tile
       int kt = 0;          // key tiles (all items): K and V phases
       int c0 = 0, c1 = 0;  // score tiles of tile 0 / 1: s_full, p_full phases (two tiles)
@@ -524,7 +691,9 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         edges ^= 1u << vs;
         return wait_bounded(&v_ready[vs], ~(edges >> vs) & 1, abort_flag);
       };
-      while (ok && walk.next(p, it)) {
+      while (ok && pg_item(queue, i_full, n, abort_flag)) {
+        const PgItem it = queue.it[n % kPgItems];
+        mbar_arrive(&i_empty[n % kPgItems]);
         const bool has1 = kTiles == 2 && it.tokens > p.TQ;
         if (!(ok = wait_bounded(q_full, n & 1, abort_flag))) break;
         if constexpr (kTiles == 1) {
@@ -532,7 +701,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           auto scores = [&](int j, int kn) {
             if (!wait_bounded(&k_full[kn & 1], (kn >> 1) & 1, abort_flag)) return false;
             tc_fence_after();
-            issue_s((kn & 1) ? tS1 : tS0, dQ0, kn & 1, pg_tile(it, it.tile(j)).n);
+            issue_s((kn & 1) ? tS1 : tS0, dQ0, kn & 1, it.width(it.tile(j)));
             umma_commit(&s_full[kn & 1]);
             umma_commit(&k_empty[kn & 1]);
             if (j == it.count() - 1) umma_commit(q_empty);
@@ -541,9 +710,8 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           if (!(ok = scores(0, kt))) break;
           if (it.count() > 1 && !(ok = scores(1, kt + 1))) break;
           for (int j = 0; j < it.count(); ++j, ++kt) {
-            const PgTile tl = pg_tile(it, it.tile(j));
-            const int w = tl.n;
-            if (!(ok = wait_v(tl.edge()))) break;
+            const int t = it.tile(j), w = it.width(t);
+            if (!(ok = wait_v(it.edge(t)))) break;
             if (!(ok = wait_bounded(&p_full[kt & 1], (kt >> 1) & 1, abort_flag))) break;
             if (j == 0 && n > 0 && !(ok = wait_bounded(&o_empty[0], (n - 1) & 1, abort_flag))) break;
             tc_fence_after();
@@ -556,7 +724,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           if (!(ok = wait_bounded(&k_full[kt & 1], (kt >> 1) & 1, abort_flag))) break;
           tc_fence_after();
           {
-            const int w = pg_tile(it, it.tile(0)).n;
+            const int w = it.width(it.tile(0));
             issue_s(tS0, dQ0, kt & 1, w);
             umma_commit(&s_full[0]);
             if (has1) {
@@ -568,9 +736,8 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           }
           for (int j = 0; j < it.count(); ++j, ++kt) {
             const bool last = j == it.count() - 1;
-            const PgTile tl = pg_tile(it, it.tile(j));
-            const int w = tl.n, wn = last ? 0 : pg_tile(it, it.tile(j + 1)).n;
-            if (!(ok = wait_v(tl.edge()))) break;
+            const int t = it.tile(j), w = it.width(t), wn = it.width(it.tile(j + 1));
+            if (!(ok = wait_v(it.edge(t)))) break;
             if (!(ok = wait_bounded(&p_full[0], c0 & 1, abort_flag))) break;
             // O_0 is free once the previous item's epilogue has read it
             if (j == 0 && n > 0 && !(ok = wait_bounded(&o_empty[0], (n - 1) & 1, abort_flag))) break;
@@ -620,22 +787,13 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     int n = 0;   // items this tile slot took part in
     int tg = 0;  // score tiles it consumed
     bool ok = true;
-    // The walk and the item live in shared memory, one copy per warp: the loop
-    // over key tiles needs every register.
-    struct Items {
-      PgWalk<kTiles> walk;
-      PgItem it;
-    };
-    static_assert(sizeof(Items) <= 128, "one slot per warp");
-    Items& items = *reinterpret_cast<Items*>(smem + Lay::kOffItems + warp * 128);
-    if (lane == 0) items.walk = PgWalk<kTiles>(p, plan);
-    const auto next = [&]() {  // by one lane for the warp
-      __syncwarp();
-      const int more = lane == 0 ? items.walk.next(p, items.it) : 0;
-      return __shfl_sync(0xffffffffu, more, 0) != 0;  // the item is visible after it
-    };
-    const PgItem& it = items.it;
-    while (ok && work && (kTiles == 2 || i == 0) && next()) {
+    // The item stays in shared memory: the loop over key tiles needs every register.
+    for (int item = 0; ok && work && (kTiles == 2 || i == 0) && pg_item(queue, i_full, item, abort_flag); ++item) {
+      const PgItem& it = queue.it[item % kPgItems];
+      const auto done = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&i_empty[item % kPgItems]);
+      };
       const int tokens = min(p.TQ, it.tokens - i * p.TQ);  // valid tokens of this tile
       const bool whole = it.t0 == 0 && it.t1 == it.n_kt;
       if (threadIdx.x == 0 && !whole) {
@@ -649,7 +807,10 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           desc->rows = it.tokens * p.G;
         }
       }
-      if (tokens <= 0) continue;  // no second tile
+      if (tokens <= 0) {  // no second tile
+        done();
+        continue;
+      }
       const bool row_ok = tr < tokens;
       const bool warp_ok = __any_sync(0xffffffffu, row_ok);
       const int pos0 = it.p0 + i * p.TQ, pos = pos0 + tr;
@@ -769,9 +930,19 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       tc_fence_after();
       float o[128];
       tmem_load128_sync(tO, o);
+      const bool hidden = *const_cast<volatile int*>(&queue.dirty[item % kPgItems]);
       tc_fence_before();
       mbar_arrive(&o_empty[i]);
       ++n;
+      if (hidden && row_ok) {
+        float t[128];  // a copy: the call takes an address, and O stays in registers otherwise
+#pragma unroll
+        for (int e = 0; e < 128; ++e) t[e] = o[e];
+        pg_add_hidden(p, it, it.start + it.t0 * kPgKeys, it.start + it.t1 * kPgKeys, it.tok0 + i * p.TQ + tr, h, pos, m,
+                      0, t);
+#pragma unroll
+        for (int e = 0; e < 128; ++e) o[e] = t[e];
+      }
       if (row_ok && !whole) {
         const size_t slot = (size_t)blockIdx.x * 2 + (it.t0 == 0 ? 1 : 0);
         const size_t row = slot * (kTiles * 128) + i * 128 + r;
@@ -820,9 +991,10 @@ __global__ void __launch_bounds__(kPgThreads, 1)
             }
           }
           if (p.lse)
-            p.lse[(size_t)h * p.pb.total_q + tok] = (l > 0.f) ? (m * 0.6931471805599453f + logf(l)) : -INFINITY;
+            p.lse[(size_t)h * p.pb.total_q + tok] = (l != 0.f) ? (m * 0.6931471805599453f + logf(l)) : -INFINITY;
         }
       }
+      done();
     }
   }
 
@@ -931,7 +1103,7 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedAttnParam
     else
       reinterpret_cast<uint2*>(p.out)[ob] = make_uint2(pack_bf16(acc.x * f, acc.y * f), pack_bf16(acc.z * f, acc.w * f));
     if (p.lse && lane == 0)
-      p.lse[(size_t)h * p.pb.total_q + tok] = (Z > 0.f) ? (M * 0.6931471805599453f + logf(Z)) : -INFINITY;
+      p.lse[(size_t)h * p.pb.total_q + tok] = (Z != 0.f) ? (M * 0.6931471805599453f + logf(Z)) : -INFINITY;
   }
 }
 

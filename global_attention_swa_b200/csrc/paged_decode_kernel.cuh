@@ -1,16 +1,15 @@
-// Attention over a paged cache where each sequence brings at most 16 rows
-// (tokens x query heads of a key/value head): the decode step, and a few
-// drafted tokens where fewer heads share a key/value head.
+// The decode step over a paged cache: one new token per sequence and at most 16
+// query heads to a key/value head.
 //
-// Bound by the cache's bytes: 16 rows do 32 flop for a byte of K and V, which
+// Bound by the cache's bytes: 16 rows do 16 flop for a byte of K and V, which
 // the warp-level mma.sync.m16n8k16 carries while the bytes stream in; a
 // tcgen05 tile would spend its 128 rows on them.  So a CTA is small, two share
 // an SM (2 x 80 KB of keys and values in flight), and one's merge and epilogue
 // overlap the other's loads.
 //
 // The items, their cuts and the combine kernel are those of
-// paged_attention_kernel with a tile of 16 rows: one item is one key/value
-// head of one sequence.
+// paged_attention_kernel with a tile of one token's rows: an item is one
+// key/value head of one sequence.
 //
 //   warp 4      loads: K and V in tiles of 64 keys through two stages (TMA, a
 //               lane per box; the page table is looked up here), Q rows ahead
@@ -46,7 +45,7 @@ static_assert(2 * (kPdSmemBytes + 1024) <= 228 * 1024, "two CTAs to an SM");
 
 __global__ void __launch_bounds__(kPdThreads, 2)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                        const __nv_bfloat16* __restrict__ q, const PagedAttnParams p) {
+                        const __grid_constant__ PagedAttnParams p) {
   extern __shared__ __align__(1024) uint8_t pdsmem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(pdsmem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kPdOffBar);
@@ -106,12 +105,11 @@ __global__ void __launch_bounds__(kPdThreads, 2)
       look_up();
       const int qb = n & 1;
       if (n >= 2 && !(ok = wait_warp(&q_empty[qb], ((n >> 1) - 1) & 1, abort_flag))) break;
-      const int rows = it.tokens * p.G;
-      if (lane == 0) mbar_arrive_expect_tx(&q_full[qb], rows * 384);
+      if (lane == 0) mbar_arrive_expect_tx(&q_full[qb], p.G * 384);
       __syncwarp();
-      if (lane < rows) {
-        const size_t at = (size_t)(it.tok0 + lane / p.G) * p.Hq + it.g * p.G + lane % p.G;
-        bulk_load(smem + kPdOffQ + qb * kPdQBytes + lane * kPdQRow, q + at * 192, 384, &q_full[qb]);
+      if (lane < p.G) {
+        const size_t at = (size_t)it.tok0 * p.Hq + it.g * p.G + lane;
+        bulk_load(smem + kPdOffQ + qb * kPdQBytes + lane * kPdQRow, p.q + at * 192, 384, &q_full[qb]);
       }
       ++n;
       while (k0 < end) {
@@ -141,14 +139,14 @@ __global__ void __launch_bounds__(kPdThreads, 2)
     return;
   }
   // -------------------------------------------------------------- consumers
-  const int r0 = lane >> 2;       // rows r0 and r0 + 8: row = token * G + head
+  const int r0 = lane >> 2;       // rows (heads) r0 and r0 + 8
   const int cq = (lane & 3) * 2;  // column pair within an 8-wide block
   const int kw = warp * 16;       // this warp's 16 keys of each tile
   const uint32_t sbase = smem_u32(smem);
   int n = 0, kt = 0;
   bool ok = true;
   while (ok && walk.next(p, it)) {
-    const int rows = it.tokens * p.G;
+    const int rows = p.G;
     const int qb = n & 1;
     uint32_t qa[12][4];
     if ((ok = wait_bounded(&q_full[qb], (n >> 1) & 1, abort_flag))) {
@@ -163,9 +161,6 @@ __global__ void __launch_bounds__(kPdThreads, 2)
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_empty[qb]);
     }
-    // keys that the two rows see: [lo, hi]
-    const int pos0 = it.p0 + min(r0, rows - 1) / p.G, pos1 = it.p0 + min(r0 + 8, rows - 1) / p.G;
-    const int lo0 = p.window > 0 ? max(0, pos0 - p.window + 1) : 0, lo1 = p.window > 0 ? max(0, pos1 - p.window + 1) : 0;
     float o[16][4];
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[e][0] = o[e][1] = o[e][2] = o[e][3] = 0.f;
@@ -199,10 +194,11 @@ __global__ void __launch_bounds__(kPdThreads, 2)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int key = kpos + (e >> 1) * 8 + cq + (e & 1);
+          const bool seen = key < end && key >= it.lo;  // all rows are the same token's
           float& a = s[e >> 1][e & 1];
           float& b = s[e >> 1][2 + (e & 1)];
-          a = (key <= pos0 && key >= lo0) ? a * p.scale_log2 : -INFINITY;
-          b = (key <= pos1 && key >= lo1) ? b * p.scale_log2 : -INFINITY;
+          a = seen ? a * p.scale_log2 : -INFINITY;
+          b = seen ? b * p.scale_log2 : -INFINITY;
           mx0 = fmaxf(mx0, a);
           mx1 = fmaxf(mx1, b);
         }
@@ -346,7 +342,7 @@ __global__ void __launch_bounds__(kPdThreads, 2)
       }
     }
     if (ok && row < rows) {
-      const int tok = it.tok0 + row / p.G, h = it.g * p.G + row % p.G;
+      const int tok = it.tok0, h = it.g * p.G + row;
       if (!whole) {
         const size_t at = ((size_t)blockIdx.x * 2 + (it.t0 == 0 ? 1 : 0)) * kPdRows + row;
         if (MIMO_ROW_OK(at, (long long)gridDim.x * 2 * kPdRows)) {
@@ -372,7 +368,7 @@ __global__ void __launch_bounds__(kPdThreads, 2)
                 make_uint2(pack_bf16(acc[j].x * f, acc[j].y * f), pack_bf16(acc[j].z * f, acc[j].w * f));
         }
         if (p.lse && (tid & 7) == 0)
-          p.lse[(size_t)h * p.pb.total_q + tok] = (Lf > 0.f) ? (Mf * 0.6931471805599453f + logf(Lf)) : -INFINITY;
+          p.lse[(size_t)h * p.pb.total_q + tok] = (Lf != 0.f) ? (Mf * 0.6931471805599453f + logf(Lf)) : -INFINITY;
       }
     }
     ++n;

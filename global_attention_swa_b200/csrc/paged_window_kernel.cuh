@@ -15,8 +15,8 @@
 //   warp 12     loads Q (two buffers, a block ahead) and K (once per item, a
 //               lane per box of 16 keys; the page table is looked up here)
 //   warp 13     MMA issuer: S(n) = Q K^T into score buffer n & 1, then O = P(n-1) V
-//   warp 14     loads V (once per item, as K) and zeroes the value rows that
-//               nothing of the item sees
+//   warp 14     loads V (once per item, as K) and zeroes its rows that nothing sees
+//   warp 15     works out the items of this CTA's share, ahead of the others
 //   warps 0-7   softmax: warpgroup s takes the blocks with n & 1 == s, one row
 //               per thread, one pass over its TMEM row
 //   warps 8-11  epilogue: O / l -> out, lse
@@ -36,7 +36,7 @@
 
 namespace mimo {
 
-constexpr int kPwThreads = 480;
+constexpr int kPwThreads = 512;
 constexpr int kPwKeys = 160;
 constexpr int kPwBoxRows = 16;
 constexpr int kPwKBox = kPwKeys * 128;                // [keys][64 dims], 1024-aligned
@@ -46,26 +46,64 @@ constexpr int kPwOffV = kPwOffK + 3 * kPwKBox;        // 2 boxes
 constexpr int kPwOffOnes = kPwOffV + 2 * kPwKBox;     // the third value block: ones
 constexpr int kPwOffML = kPwOffOnes + kPwKBox;        // [2][128] float4 (m, l, sink term, -)
 constexpr int kPwOffBar = kPwOffML + 2 * 128 * 16;
-constexpr int kPwSmemBytes = kPwOffBar + 512 + 1024;  // barriers, plan; alignment slack
+constexpr int kPwOffItems = kPwOffBar + 512;            // barriers and plan before it
+constexpr int kPwSmemBytes = kPwOffItems + 512 + 1024;  // the queue of items; alignment slack
+constexpr int kPwReaders = 3 + 8 + 4;                   // warps 12, 13, 14, softmax, epilogue
 constexpr uint32_t kPwColO = 2 * kPwKeys, kPwColSum = kPwColO + 128;
 static_assert(kPwOffOnes % 1024 == 0 && kPwColSum + 16 <= 512 && kPwSmemBytes <= 227 * 1024, "window layout");
 
-// An item's keys: the first one loaded, how many (a multiple of 16), and the
-// rows [0, zlo) and [zhi, n) of them that nothing sees.
-__device__ __forceinline__ PgTile pw_keys(const PgItem& it) {
-  PgTile r;
-  r.k0 = it.start;
-  const int left = it.hi + 1 - it.start;
-  r.n = (left + 15) & ~15;
-  r.zlo = it.lo - it.start;
-  r.zhi = left;
-  return r;
+// An item's keys, all in one tile.
+__device__ __forceinline__ PgTile pw_keys(const PgItem& it) { return pg_keys(it, it.start, kPwKeys); }
+
+// One row (packed row tok, head h, position pos) from the definition, its output
+// only: keys that it does not see take no part at all.  For rows whose product
+// over the item's keys is not finite.  (Looking the values over as they come
+// instead, one warp ahead of the products, cost 23 us of a 69 us call; a test of
+// the products, 2 at most.)
+__device__ __noinline__ void pw_row_again(const PagedAttnParams& p, const PgItem& it, int tok, int h, int pos) {
+  if (!MIMO_ROW_OK((long long)tok * p.Hq + h, (long long)p.pb.total_q * p.Hq)) return;
+  const uint32_t* q = reinterpret_cast<const uint32_t*>(p.q + ((size_t)tok * p.Hq + h) * 192);
+  float m = p.sinks ? p.sinks[h] * 1.4426950408889634f : -INFINITY;
+  float l = p.sinks ? 1.f : 0.f;
+  float o[128];
+#pragma unroll 1
+  for (int d = 0; d < 128; ++d) o[d] = 0.f;
+#pragma unroll 1
+  for (int j = max(0, pos - p.window + 1); j <= pos; ++j) {
+    const int e = p.pb.table[(size_t)it.b * p.pb.max_pages + j / p.pb.page_size];
+    const bool page = e >= 0 && e < p.pb.num_pages;  // without one: zero key and value
+    const size_t row = page ? ((size_t)e * p.pb.page_size + j % p.pb.page_size) * p.Hkv + it.g : 0;
+    const uint32_t* k = reinterpret_cast<const uint32_t*>(p.k + row * 192);
+    const uint32_t* v = reinterpret_cast<const uint32_t*>(p.v + row * 128);
+    float s = 0.f;
+#pragma unroll 1
+    for (int i = 0; page && i < 96; ++i) s += bf16_lo(q[i]) * bf16_lo(k[i]) + bf16_hi(q[i]) * bf16_hi(k[i]);
+    s *= p.scale_log2;
+    const float up = fmaxf(m, s), neg = up == -INFINITY ? 0.f : -up;
+    const float f = ex2(m + neg), pe = ex2(s + neg);
+    m = up;
+    l = l * f + pe;
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i) {
+      o[2 * i] = o[2 * i] * f + (page ? pe * bf16_lo(v[i]) : 0.f);
+      o[2 * i + 1] = o[2 * i + 1] * f + (page ? pe * bf16_hi(v[i]) : 0.f);
+    }
+  }
+  const float f = l != 0.f ? p.v_scale / l : 0.f;
+  const size_t ob = ((size_t)tok * p.Hq + h) * 128;
+#pragma unroll 1
+  for (int d = 0; d < 128; ++d) {
+    if (p.out_f32)
+      reinterpret_cast<float*>(p.out)[ob + d] = o[d] * f;
+    else
+      reinterpret_cast<__nv_bfloat16*>(p.out)[ob + d] = __float2bfloat16_rn(o[d] * f);
+  }
 }
 
 template <int kBlocks>
 __global__ void __launch_bounds__(kPwThreads, 1)
     paged_window_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                        const __grid_constant__ CUtensorMap tm_v, const PagedAttnParams p) {
+                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedAttnParams p) {
   extern __shared__ __align__(1024) uint8_t pwsmem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(pwsmem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kPwOffBar);
@@ -86,8 +124,11 @@ __global__ void __launch_bounds__(kPwThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 21);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 22);
   volatile int* never_flag = reinterpret_cast<volatile int*>(bars + 23);  // never raised
-  PgPlace* plan = reinterpret_cast<PgPlace*>(bars + 24);          // [2]
-  long long* warp_sum = reinterpret_cast<long long*>(bars + 28);  // [15]
+  PgPlace* plan = reinterpret_cast<PgPlace*>(bars + 26);          // [2]
+  uint64_t* i_full = bars + 30;                                   // [kPgItems]
+  uint64_t* i_empty = bars + 34;                                  // [kPgItems]
+  long long* warp_sum = reinterpret_cast<long long*>(bars + 38);  // [16]
+  PgQueue& queue = *reinterpret_cast<PgQueue*>(smem + kPwOffItems);
   float4* ml = reinterpret_cast<float4*>(smem + kPwOffML);  // [2][128] (m, l, sink term) per row
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -118,6 +159,10 @@ __global__ void __launch_bounds__(kPwThreads, 1)
       mbar_init(v_ready, 1);
       mbar_init(o_full, 1);
       mbar_init(o_empty, 128);
+      for (int i = 0; i < kPgItems; ++i) {
+        mbar_init(&i_full[i], 1);
+        mbar_init(&i_empty[i], kPwReaders);
+      }
       mbar_init(mma_drain, 1);
       *never_flag = 0;
       *abort_flag = timed_out_before() ? 1 : 0;
@@ -134,10 +179,18 @@ __global__ void __launch_bounds__(kPwThreads, 1)
   const uint32_t sbase = smem_u32(smem);
   const bool work = share && !*abort_flag;
 
-  // Each role walks the same items, and the blocks of each: block n of the
+  // Each role takes the same items in turn, and the blocks of each: block n of the
   // CTA's uses buffer n & 1.
-  PgWalk<kBlocks> walk(p, plan);
+  int items = 0;  // taken by this role
   PgItem it;
+  const auto next = [&](bool warp_wide) {  // the item is copied and released at once
+    if (!pg_item(queue, i_full, items, abort_flag)) return false;
+    it = queue.it[items % kPgItems];
+    if (warp_wide) __syncwarp();
+    if (!warp_wide || lane == 0) mbar_arrive(&i_empty[items % kPgItems]);
+    ++items;
+    return true;
+  };
   const auto blocks_of = [&](const PgItem& x) { return kBlocks == 2 && x.tokens > p.TQ ? 2 : 1; };
 
   if (!work) {
@@ -154,7 +207,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
       }
       ++armed_q;
     };
-    bool ok = true, have = walk.next(p, it);
+    bool ok = true, have = next(true);
     int n = 0, kp = 0;
     if (have) load_q(it, 0, 0);
     PgTile keys = pw_keys(it);
@@ -181,7 +234,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         const int bn = (n + 1) & 1;
         const bool in_item = blk + 1 < nblk;
         if (!in_item) {
-          have = walk.next(p, it);
+          have = next(true);
           if (!have) continue;
           keys = pw_keys(it);
           boxes = keys.n / kPwBoxRows;
@@ -219,7 +272,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
       int n = 0, kp = 0;
       int pm = -1, pkp = 0, pk = 0;  // previous block: number, item, keys
       bool pfirst = false, plast = false;
-      while (ok && walk.next(p, it)) {
+      while (ok && next(false)) {
         const int nblk = blocks_of(it), k = pw_keys(it).n;
         const uint32_t idesc_s = idesc_bf16_f32(128, 0, false, false) | (static_cast<uint32_t>(k >> 3) << 17);
         for (int blk = 0; ok && blk < nblk; ++blk, ++n) {
@@ -251,7 +304,8 @@ __global__ void __launch_bounds__(kPwThreads, 1)
   } else if (warp == 14) {
     // ------------------------------------------------------------ V, and its rows nothing sees
     int kp = 0;
-    while (walk.next(p, it)) {
+    while (pg_item(queue, i_full, kp, abort_flag)) {
+      const PgItem it = queue.it[kp % kPgItems];
       const PgTile keys = pw_keys(it);
       const int boxes = keys.n / kPwBoxRows;
       const int row = lane < boxes ? pg_box_row(p, it, keys, lane) : 0;
@@ -265,17 +319,19 @@ __global__ void __launch_bounds__(kPwThreads, 1)
           tma_load_3d(smem + kPwOffV + c * kPwKBox + lane * kPwBoxRows * 128, &tm_v, v_full, c * 64, it.g, row);
       }
       if (!wait_warp(v_full, kp & 1, abort_flag)) break;
-      const int rows = keys.zlo + keys.n - keys.zhi;
-      for (int w = lane; w < rows * 16; w += 32) {  // 16 vectors a row: 8 in each 64-column box
-        const int i = w >> 4, r = i < keys.zlo ? i : keys.zhi + (i - keys.zlo);
-        *reinterpret_cast<uint4*>(smem + kPwOffV + ((w >> 3) & 1) * kPwKBox + r * 128 + (w & 7) * 16) =
-            make_uint4(0, 0, 0, 0);
+      if (keys.zlo > 0 || keys.zhi < keys.n) {
+        pg_zero_unseen(keys, sbase + kPwOffV, kPwKBox);
+        fence_proxy_async_smem();
+        __syncwarp();
       }
-      if (rows > 0) fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(v_ready);
+      if (lane == 0) {
+        mbar_arrive(v_ready);
+        mbar_arrive(&i_empty[kp % kPgItems]);
+      }
       ++kp;
     }
+  } else if (warp == 15) {
+    if (lane == 0) pg_schedule<kBlocks>(p, plan, queue, i_full, i_empty, abort_flag);
   } else if (warp < 8) {
     // ------------------------------------------------------------ softmax
     const int s = warp >> 2;               // this warpgroup's blocks: n & 1 == s
@@ -284,7 +340,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     int n = 0;
     bool ok = true;
-    while (ok && walk.next(p, it)) {
+    while (ok && next(true)) {
       const int nblk = blocks_of(it);
       const PgTile keys = pw_keys(it);
       const int N = keys.n;
@@ -382,7 +438,8 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     const uint32_t tO = tbase + lane_off + kPwColO;
     int n = 0;
     bool ok = true;
-    while (ok && walk.next(p, it)) {
+    for (int item = 0; ok && pg_item(queue, i_full, item, abort_flag); ++item) {
+      const PgItem& it = queue.it[item % kPgItems];
       const int nblk = blocks_of(it);
       for (int blk = 0; ok && blk < nblk; ++blk, ++n) {
         const int b = n & 1;
@@ -400,7 +457,8 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                           MIMO_ROW_OK((long long)tok * p.Hq + hg, (long long)p.pb.total_q * p.Hq);
         const float f = (lr > 0.f) ? p.v_scale / lr : 0.f;
         const size_t ob = ((size_t)tok * p.Hq + hg) * 128;
-        // O in two 64-column halves (480 threads leave 136 registers each); it is
+        float odd = 0.f;  // NaN once a value of O is not finite
+        // O in two 64-column halves (512 threads leave 128 registers each); it is
         // released to the next P V after the second half is in registers
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
@@ -411,6 +469,8 @@ __global__ void __launch_bounds__(kPwThreads, 1)
             mbar_arrive(o_empty);
           }
           if (!live) continue;
+#pragma unroll
+          for (int e = 0; e < 64; ++e) odd = fmaf(o[e], 0.f, odd);
           if (p.out_f32) {
             float* dst = reinterpret_cast<float*>(p.out) + ob + h * 64;
 #pragma unroll
@@ -442,10 +502,15 @@ __global__ void __launch_bounds__(kPwThreads, 1)
             }
           }
         }
+        // 0 * v is NaN where v is not finite, so such a value of a key that the row
+        // does not see, and another row of the item does, is in its sum
+        if (odd != 0.f) pw_row_again(p, it, tok, hg, it.p0 + blk * p.TQ + a);
         if (live && p.lse)
           p.lse[(size_t)hg * p.pb.total_q + tok] =
-              (mlv.y > 0.f) ? (mlv.x * 0.6931471805599453f + logf(mlv.y)) : -INFINITY;
+              (mlv.y != 0.f) ? (mlv.x * 0.6931471805599453f + logf(mlv.y)) : -INFINITY;
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&i_empty[item % kPgItems]);
     }
   }
 

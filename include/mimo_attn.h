@@ -371,11 +371,10 @@ size_t mimo_attn_paged_attention_workspace_size(const mimo_attn_dims_t* dims, in
  *                aligned (may be NULL when that size is 0); its contents need no
  *                preparation.  Calls sharing one workspace must not overlap on the GPU.
  *
- * Hq / Hkv <= 128.  Slots that no query of the sequence sees (past its length,
- * behind its window) may hold anything, NaN included, and their table entries
- * may be negative: they are not read into the result.  A key or value that some
- * queries of the chunk see and others do not must be finite.  A visible entry
- * without a page reads as zero keys and values.
+ * Hq / Hkv <= 128.  A key that a query does not see (later in the chunk, behind
+ * its window, past the length) has no influence on it, whatever its slot holds,
+ * NaN and infinities included; a table entry wholly out of the sequence's sight
+ * may be negative.  A visible entry without a page reads as zero keys and values.
  */
 mimo_status_t mimo_attn_paged_attention(const mimo_attn_dims_t* dims, const void* q, const void* k_pages,
                                         const void* v_pages, const int32_t* block_table,

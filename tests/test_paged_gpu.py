@@ -230,6 +230,37 @@ def test_a_visible_entry_without_a_page_reads_as_zeros(bad, n):
     check(out, lse, ref)
 
 
+@pytest.mark.parametrize("lens,news,window,hq,hkv", [
+    ([200], [5], 0, 16, 1), ([200, 90], [40, 33], 0, 16, 1), ([3000], [30], 0, 16, 1), ([200, 40], [40, 9], 129, 16, 1),
+    ([300], [40], 200, 16, 1), ([200], [7], 3, 16, 1), ([700], [300], 0, 2, 2), ([500], [200], 10, 2, 2),
+    ([150, 70], [12, 3], 0, 8, 2), ([700], [90], 600, 16, 1)])
+@pytest.mark.parametrize("what", [float("nan"), float("inf"), float("-inf")])
+def test_values_that_are_not_finite_reach_only_the_rows_that_see_them(lens, news, window, hq, hkv, what):
+    """Not finite: some value columns of one key, all of another, one key's own row; each
+    seen by some queries of the chunk and hidden from others."""
+    x = build(lens, news, window, 16, hq, hkv, seed=17)
+    for b, (L, n) in enumerate(zip(lens, news)):
+        first = L - n
+        low = max(0, first - window + 1) if window else 0
+        spots = [(first + n // 2, "v", slice(3, 9)), (L - 1, "v", slice(None)), (first + 3 * n // 4, "k", slice(0, 1))]
+        if window:
+            spots.append((low + min(n, window) // 2, "v", slice(100, 101)))
+        for p, kind, cols in spots:
+            page, slot = int(x["table"][b, p // 16]), p % 16
+            x["kp" if kind == "k" else "vp"][page, slot, 0, cols] = what
+    want, want_lse, mass = oracle_of(x)
+    out, lse = attend(x, out_dtype=torch.float32)
+    o, l = P.to64(out), P.to64(lse)
+    fine, lfine = np.isfinite(want), np.isfinite(want_lse)
+    assert not fine.all() and fine[:, :, 50].any()
+    assert np.array_equal(np.isfinite(o), fine)
+    bound = 2.0 ** -8 * (mass + np.abs(want)) + 5.2e-4 * mass + 1e-6
+    ok = fine & np.isfinite(mass)
+    assert np.all(np.abs(o - want)[ok] <= bound[ok])
+    assert np.array_equal(np.isnan(l), np.isnan(want_lse)) and np.array_equal(np.isfinite(l), lfine)
+    assert np.max(np.abs(l - want_lse)[lfine], initial=0.0) <= 3e-4
+
+
 def test_agrees_with_prefill_and_decode():
     """The whole prompt as one chunk is the dense prefill; its last token alone is the dense decode."""
     T, hq, hkv = 321, 64, 4

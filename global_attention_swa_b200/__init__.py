@@ -493,6 +493,23 @@ def _call(fn, dev, *args):
         _check(status)
 
 
+def _int(x, name):
+    """x as the C int that the library takes (ctypes would cut it to 32 bits)."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} is out of range (got {x})")
+    return x
+
+
+def _other_stream(stream, *tensors):
+    """Tensors allocated here on the current stream and used on ``stream``: their memory is
+    not given out again before ``stream`` is past the call."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
 def _paged_pools(k_pages, v_pages, block_table):
     """(num_pages, page_size, Hkv, Dqk, Dv, num_seqs, max_pages) of a paged cache."""
     if k_pages.dim() != 4 or v_pages.dim() != 4:
@@ -520,7 +537,7 @@ def mimo_attn_paged_attention(q, k_pages, v_pages, block_table, cu_seqlens_q, se
 
     Returns (out [Nt,Hq,128], lse [Hq,Nt] fp32 or None).
     """
-    if _fast is not None and stream is None:
+    if _fast is not None and stream is None and (out is not None or out_dtype in _OUT):
         r = _fast.paged_attention(q, k_pages, v_pages, block_table, cu_seqlens_q, seqlens, max_seqlen_q, window,
                                   sinks, out, lse, workspace, (out_dtype if out is None else out.dtype) is _F32,
                                   0.0 if softmax_scale is None else softmax_scale, v_scale, return_lse)
@@ -538,8 +555,9 @@ def mimo_attn_paged_attention(q, k_pages, v_pages, block_table, cu_seqlens_q, se
         out = q.new_empty((nt, hq, dv), dtype=out_dtype)
     if lse is None and return_lse:
         lse = q.new_empty((hq, nt), dtype=_F32)
-    max_seqlen_q, window = int(max_seqlen_q), int(window)
-    dims = _dims_ref(hq, hkv, dqk, dv, softmax_scale, v_scale, out.dtype)
+    max_seqlen_q, window = _int(max_seqlen_q, "max_seqlen_q"), _int(window, "window")
+    dims = _dims_ref(hq, hkv, dqk, dv, None if softmax_scale is None else float(softmax_scale), float(v_scale),
+                     out.dtype)
     need = lib.mimo_attn_paged_attention_workspace_size(dims, B, nt, max_seqlen_q, window)
     ws = wbytes = 0
     if workspace is not None:
@@ -551,6 +569,7 @@ def mimo_attn_paged_attention(q, k_pages, v_pages, block_table, cu_seqlens_q, se
     _call(lib.mimo_attn_paged_attention, dev, dims, *addrs, B, nt, max_seqlen_q, P, ps, M, window, sink,
           _addr(out, "out", out.dtype if out.dtype in _OUT else _OUT, (nt, hq, dv), dev),
           _addr(lse, "lse", _F32, (hq, nt), dev), ws, wbytes, stream)
+    _other_stream(stream, out, lse, workspace)
     return out, lse
 
 
@@ -575,7 +594,8 @@ def mimo_attn_paged_append(q, k_new, v_new, k_pages, v_pages, block_table, cu_se
           _addr(v_pages, "v_pages", _BF16, (P, ps, hkv, dv), dev),
           _addr(block_table, "block_table", _I32, (B, M), dev),
           _addr(cu_seqlens_q, "cu_seqlens_q", _I32, (B + 1,), dev), _addr(seqlens, "seqlens", _I32, (B,), dev),
-          B, nt, P, ps, M, float(rope_theta), dqk if rotary_dim is None else int(rotary_dim), stream)
+          B, nt, P, ps, M, float(rope_theta), dqk if rotary_dim is None else _int(rotary_dim, "rotary_dim"), stream)
+    _other_stream(stream, q_out)
     return q_out
 
 
@@ -617,11 +637,12 @@ def mimo_attn_page_hold(page_refs, block_table, seqlens, page_size, first=None, 
     info = page_refs.new_empty((2,)) if info is None else info
     ws, ws_addr, ws_bytes = _page_workspace(workspace, lib.mimo_attn_page_hold_workspace_size(P), page_refs)
     _call(lib.mimo_attn_page_hold, dev, _addr(page_refs, "page_refs", _I32, (P,), dev), P,
-          _addr(block_table, "block_table", _I32, (B, M), dev), B, M, int(page_size),
+          _addr(block_table, "block_table", _I32, (B, M), dev), B, M, _int(page_size, "page_size"),
           _addr(seqlens, "seqlens", _I32, (B,), dev), _addr(first, "first", _I32, (B,), dev),
           _addr(write_from, "write_from", _I32, (B,), dev), _addr(refs_out, "refs_out", _I32, (P,), dev),
           _addr(table_out, "table_out", _I32, (B, M), dev), _addr(moves, "moves", _I32, (B, 2), dev),
           _addr(info, "info", _I32, (2,), dev), ws_addr, ws_bytes, stream)
+    _other_stream(stream, refs_out, table_out, moves, info, ws)
     return refs_out, table_out, moves, info
 
 
@@ -643,6 +664,7 @@ def mimo_attn_page_fork(page_refs, block_table, parent, refs_out=None, table_out
     _call(lib.mimo_attn_page_fork, dev, _addr(page_refs, "page_refs", _I32, (P,), dev), P,
           _addr(block_table, "block_table", _I32, (B, M), dev), B, M, _addr(parent, "parent", _I32, (n,), dev), n,
           _addr(refs_out, "refs_out", _I32, (P,), dev), _addr(table_out, "table_out", _I32, (n, M), dev), stream)
+    _other_stream(stream, refs_out, table_out)
     return refs_out, table_out
 
 
@@ -659,7 +681,7 @@ def mimo_attn_page_compact(page_refs, block_table, max_moves, refs_out=None, tab
         if r is not None:
             return _taken(r)
     P, B, M = _page_table(page_refs, block_table)
-    max_moves = int(max_moves)
+    max_moves = _int(max_moves, "max_moves")
     dev = page_refs.device
     refs_out = page_refs.new_empty((P,)) if refs_out is None else refs_out
     table_out = page_refs.new_empty((B, M)) if table_out is None else table_out
@@ -671,6 +693,7 @@ def mimo_attn_page_compact(page_refs, block_table, max_moves, refs_out=None, tab
           _addr(refs_out, "refs_out", _I32, (P,), dev), _addr(table_out, "table_out", _I32, (B, M), dev),
           _addr(moves, "moves", _I32, (max_moves, 2), dev), _addr(info, "info", _I32, (2,), dev), ws_addr,
           ws_bytes, stream)
+    _other_stream(stream, refs_out, table_out, moves, info, ws)
     return refs_out, table_out, moves, info
 
 

@@ -110,7 +110,7 @@ struct Args {
   int integer(int i) {
     if (!plain) return 0;
     const long v = PyLong_Check(a[i]) ? PyLong_AsLong(a[i]) : LONG_MIN;
-    if (v < INT_MIN || v > INT_MAX) {
+    if (v < INT_MIN || v > INT_MAX || PyErr_Occurred()) {
       PyErr_Clear();
       plain = false;
     }
@@ -183,7 +183,7 @@ PyObject* paged_attention(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
   if (!a.plain || hkv <= 0) MIMO_NOT_PLAIN();
   at::Tensor out, lse, ws;
   void* op = a.output(9, f32 ? kF32 : kBF16, {nt, hq, dv}, out);
-  void* ep = argv[15] == Py_True || argv[10] != Py_None ? a.output(10, kF32, {hq, nt}, lse) : nullptr;
+  void* ep = PyObject_IsTrue(argv[15]) == 1 || argv[10] != Py_None ? a.output(10, kF32, {hq, nt}, lse) : nullptr;
   size_t bytes;
   void* wp = a.workspace(11, g_attention_ws(&d, (int)B, (int)nt, most, window), ws, bytes);
   if (!a.plain) MIMO_NOT_PLAIN();

@@ -54,11 +54,12 @@ class PagedCache:
         self.page_size, self.window, self.rollback = page_size, window, rollback
         self.capacity = max_pages * page_size
 
-    def _first(self, lens, more):
-        """First position that queries from lens - more on see; never one already released."""
+    def _first(self):
+        """First position that queries from ``rollback`` before the present lengths on see;
+        never one already released."""
         if not self.window:
             return None
-        return torch.maximum(self._kept, lens - (self.window - 1 + more))
+        return torch.maximum(self._kept, self.seqlens - (self.window - 1 + self.rollback))
 
     def _hold(self, lens, first, write_from):
         _, _, moves, _ = mimo.mimo_attn_page_hold(
@@ -74,7 +75,7 @@ class PagedCache:
         would pass max_pages pages stays as it is and is recorded as an invalid
         argument in the device status.  Returns ``info``."""
         lens = self.seqlens + new_tokens
-        first = self._first(self.seqlens, self.rollback)
+        first = self._first()
         moves = self._hold(lens, first, self.seqlens)
         mimo.mimo_attn_page_copy(self.k_pages, self.v_pages, moves)
         done = (self.info[0] == 0) & (lens >= 0) & (lens <= self.capacity)
@@ -102,7 +103,8 @@ class PagedCache:
         pages behind that are released.  With a window: not below the length before the
         last ``extend`` less ``rollback``, or to 0."""
         lens = torch.minimum(lens, self.seqlens)
-        self._hold(lens, self._first(lens, 0), None)
+        # what extend kept stays, so that a later call may go back further
+        self._hold(lens, self._kept if self.window else None, None)
         self.seqlens.copy_(torch.where(lens >= 0, lens, self.seqlens))  # a negative one was recorded
         self._kept.mul_(lens != 0)
         return self.info

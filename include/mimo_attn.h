@@ -393,9 +393,10 @@ mimo_status_t mimo_attn_paged_attention(const mimo_attn_dims_t* dims, const void
  *           (may be q itself; must not overlap it otherwise)
  *   k_new   [total_q, Hkv, Dqk] bf16 before rotation;  v_new [total_q, Hkv, Dv] bf16
  *
- * Only the slots of the new positions are written.  A position without a page
- * is recorded as MIMO_ERR_INVALID_ARG: its query is rotated, its key and value
- * are not stored.
+ * Only the slots of the new positions are written; no two of them may be one
+ * slot (a page that sequences share must not be written: mimo_attn_page_hold
+ * replaces it first).  A position without a page is recorded as
+ * MIMO_ERR_INVALID_ARG: its query is rotated, its key and value are not stored.
  */
 mimo_status_t mimo_attn_paged_append(const mimo_attn_dims_t* dims, const void* q, void* q_out,
                                      const void* k_new, const void* v_new, void* k_pages, void* v_pages,

@@ -276,6 +276,29 @@ def test_other_wrappers_refuse(host):
     assert not [n for n, _ in host.calls if not n.endswith("_size")]
 
 
+@pytest.mark.parametrize("big", [2 ** 31, -2 ** 31 - 1, 2 ** 32 + 1, 2 ** 70])
+def test_whole_numbers_past_32_bits_are_refused(host, big):
+    x = _inputs()
+    att = (x["q"], x["kp"], x["vp"], x["table"], x["cu"], x["lens"])
+    for call, what in ((lambda: mimo.mimo_attn_paged_attention(*att, big, 0, x["sinks"]), "max_seqlen_q"),
+                       (lambda: mimo.mimo_attn_paged_attention(*att, 5, big, x["sinks"]), "window"),
+                       (lambda: _call_append(x, rotary_dim=big), "rotary_dim"),
+                       (lambda: mimo.mimo_attn_page_hold(x["refs"], x["table"], x["lens"], big), "page_size"),
+                       (lambda: mimo.mimo_attn_page_compact(x["refs"], x["table"], big), "max_moves")):
+        with pytest.raises(ValueError, match=what):
+            call()
+    assert not [n for n, _ in host.calls if not n.endswith("_size")]
+
+
+def test_a_scale_given_as_a_tensor_is_read_at_each_call(host):
+    scale = torch.tensor(0.5)
+    for want in (0.5, 0.25):
+        scale.fill_(want)
+        _call_attend(_inputs(), softmax_scale=scale, v_scale=2 * scale)
+        dims = host.calls[-1][1][0]._obj
+        assert (dims.softmax_scale, dims.v_scale) == (want, 2 * want)
+
+
 def test_paged_cache_refuses_sizes():
     from global_attention_swa_b200.paged_cache import PagedCache
 

@@ -702,6 +702,53 @@ def test_the_cache_keeps_its_sequences_through_bad_requests():
         assert held == [-(-n // 16) for n in lens] and int(cache.page_refs.sum()) == sum(held)
 
 
+def test_a_windowed_cache_goes_back_more_than_once():
+    """Down to the length before the last extend (less the rollback), in steps: what the
+    queries from there on see is still held, in the same pages."""
+    W, ps, rollback = 129, 16, 5
+    cache = PagedCache(1, 64, ps, 2, 40, 1, window=W, rollback=rollback)
+    cache.extend(ints([400, 300]).cuda())
+    cache.extend(ints([100, 60]).cuda())
+    table = cache.block_table.clone()
+    for back in ([500, 360], [430, 330], [400, 300], [395, 295]):
+        cache.truncate(ints(back).cuda())
+        assert cache.seqlens.tolist() == back
+        for b, L in enumerate(back):
+            for j in range((L - W + 1) // ps, -(-L // ps)):
+                assert table[b, j] >= 0 and cache.block_table[b, j] == table[b, j]
+            assert (cache.block_table[b, -(-L // ps):] < 0).all()
+    cache.truncate(ints([0, 0]).cuda())
+    assert int(cache.page_refs.sum()) == 0 and (cache.block_table < 0).all()
+    cache.extend(ints([40, 1]).cuda())
+    assert (cache.block_table >= 0).sum().item() == 4
+    mimo.mimo_attn_device_status()
+
+
+def test_arguments_that_the_native_call_leaves_to_the_binding():
+    x = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in build([40], [3], 0, 16, 8, 2, 5).items()}
+    args = [x[k] for k in ("q", "kp", "vp", "table", "cu", "lens", "most", "window", "sinks")]
+    with pytest.raises(TypeError, match="out must be"):
+        mimo.mimo_attn_paged_attention(*args, out_dtype=torch.float16)
+    with pytest.raises(TypeError, match="out must be"):
+        mimo.mimo_attn_paged_attention(*args, out=torch.empty((3, 8, 128), dtype=torch.float16, device="cuda"))
+    for big in (2 ** 31, 2 ** 32 + 3, 2 ** 70):
+        with pytest.raises(ValueError, match="max_seqlen_q"):
+            mimo.mimo_attn_paged_attention(*args[:6], big, *args[7:])
+    want = mimo.mimo_attn_paged_attention(*args)
+    got = mimo.mimo_attn_paged_attention(*args[:6], np.int64(3), *args[7:], return_lse=1)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    # a scale in a tensor, changed between two calls
+    scale, side = torch.tensor(0.5), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    seen = []
+    for v in (0.5, 0.05):
+        scale.fill_(v)
+        seen.append(mimo.mimo_attn_paged_attention(*args, softmax_scale=scale, stream=side)[0])
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(seen[-1], mimo.mimo_attn_paged_attention(*args, softmax_scale=v)[0])
+    assert not torch.equal(*seen)
+
+
 @pytest.mark.parametrize("n,window", [(1, 0), (1, 129), (5, 0), (40, 0), (40, 129)])
 def test_after_a_recorded_timeout_nothing_is_written(n, window):
     x = build([300, 60], [n, n], window, 16, 16, 1, seed=2)

@@ -929,9 +929,13 @@ mimo::PagedBatch paged_batch(const int32_t* block_table, const int32_t* cu_seqle
 
 // Which kernel a call over a paged cache takes, by the most new tokens a
 // sequence brings and the G query heads of a key/value head.
-//   decode  one token, G <= 16: warp-level MMAs, two CTAs to an SM
+//   decode  one token, G <= 16: warp-level MMAs, two CTAs to an SM (64 sequences
+//           of 1024 to 32768 keys 528 us, by tiles 536; window 129 13 and 21)
 //   window  all keys of one or two blocks of 128 / G tokens fit a score tile
-//   tile    one tile of 128 / G tokens, or two that share their key tiles
+//           (window 129, 5600 tokens: 72 us, by tiles 159; one block 79)
+//   tile    one tile of 128 / G tokens, or two that share their key tiles (1 to 6
+//           tokens at up to 16384 keys: 134 and 171 us; 2048 at 32768: 2.43 and
+//           2.28 ms)
 struct PagedVariant {
   enum Kind { decode, window, tile } kind;
   int TQ;      // tokens of a tile of rows
@@ -943,7 +947,8 @@ struct PagedVariant {
 // Under a short window an item has at most four key tiles (boxes of 16 keys:
 // the window, the item's other tokens and at most 15 keys before them), and
 // only whole items are dealt out: joining parts would cost more than the
-// shares' imbalance.
+// shares' imbalance (window 300: 5600 tokens 186 us, cut 220; 20 tokens of 4
+// sequences 14.9 and 21.5; window 129, one token of 64 sequences: 12.3 and 14.3).
 constexpr int kPagedShortWindow = 512;
 PagedVariant paged_variant(const mimo_attn_dims_t* dims, int max_seqlen_q, int window) {
   const int G = dims->num_heads_q / dims->num_heads_kv, sms = sm_count();
@@ -1129,7 +1134,6 @@ mimo_status_t mimo_attn_paged_attention(const mimo_attn_dims_t* dims, const void
   if (window > 0 && window <= kPagedShortWindow) box = 16;
   p.box_rows = box;
   p.split = v.split;
-  p.min_tiles = 2;
   p.scale_log2 = scale_log2_of(dims);
   p.v_scale = v_scale_of(dims);
   p.out_f32 = dims->out_dtype == MIMO_DTYPE_F32;

@@ -2,6 +2,11 @@
 // page_hold (a shared page that is about to be written) and page_compact ask
 // for.  Moving bytes is all it does; a CTA takes one piece of one page of one
 // layer, reads it in 16-byte vectors, several of them before the first store.
+//
+// Bound by memory bandwidth: 900 pages of 64 tokens in 6 layers, 1.77 GB read and
+// written, in 278 us: 6.36 TB/s, 97 % of a plain copy's rate (286 us with the
+// compaction that names them; with 2 and 8 vectors in flight per thread 285 and
+// 282, and 8 is the slower for few pages: 24 of 16 tokens 8.2 against 8.0 us).
 #pragma once
 
 #include "paged_common.cuh"

@@ -7,10 +7,16 @@
 // keys; loaded in boxes of 16 from the one that holds the first, that is at
 // most kPwKeys = 160 (window 129, 16 heads to a key/value head: 2 blocks of 8
 // tokens, 159).  So there is no online softmax, and the work of an item is one
-// Q K^T and one P V per block.  What bounds such a layer is its queries and outputs, 40 KB a block
-// against 100 KB of keys and values from L2 for an item, so the roles run as
-// a pipeline over blocks: while one block's softmax runs, the next one's
-// scores are computed and the queries of the one after are on their way.
+// Q K^T and one P V per block.  The bytes of such a layer are its queries and
+// outputs (80 KB a block, against 100 KB of keys and values from L2 for an item),
+// so the roles run as a pipeline over blocks: while one block's softmax runs, the
+// next one's scores are computed and the queries of the one after are on their way.
+//
+// Measured on one B200 (64 query heads, 4 key/value heads, window 129, 5600 new
+// tokens of 9 sequences, 229 MB): 72 us, 3.2 TB/s, 49 % of a plain copy's rate
+// (the general kernel: 159 us; one block to an item: 79 us).  Bound by the chain
+// of one block, scores, softmax, P V, store, of which two are under way at once:
+// TMEM holds two score tiles of 160 columns and one O.
 //
 //   warp 12     loads Q (two buffers, a block ahead) and K (once per item, a
 //               lane per box of 16 keys; the page table is looked up here)

@@ -1140,7 +1140,7 @@ mimo_status_t mimo_attn_paged_attention(const mimo_attn_dims_t* dims, const void
   p.out_v8 = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
 
   CUtensorMap tq, tk, tv;
-  if (v.kind != PagedVariant::decode) {
+  {
     const uint64_t d[3] = {192, (uint64_t)Hq, (uint64_t)total_q};
     const uint64_t s[2] = {192 * 2, (uint64_t)Hq * 192 * 2};
     const uint32_t b[3] = {64, (uint32_t)G, (uint32_t)p.TQ};
@@ -1164,7 +1164,7 @@ mimo_status_t mimo_attn_paged_attention(const mimo_attn_dims_t* dims, const void
   const int ctas = v.split ? v.ctas : (int)std::min<long>(v.ctas, items);
   const cudaStream_t cs = (cudaStream_t)stream;
   if (v.kind == PagedVariant::decode)
-    mimo::paged_decode_kernel<<<ctas, mimo::kPdThreads, mimo::kPdSmemBytes, cs>>>(tk, tv, p);
+    mimo::paged_decode_kernel<<<ctas, mimo::kPdThreads, mimo::kPdSmemBytes, cs>>>(tq, tk, tv, p);
   else if (v.kind == PagedVariant::window && v.tiles == 1)
     mimo::paged_window_kernel<1><<<ctas, mimo::kPwThreads, mimo::kPwSmemBytes, cs>>>(tq, tk, tv, p);
   else if (v.kind == PagedVariant::window)

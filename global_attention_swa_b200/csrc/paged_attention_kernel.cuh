@@ -1074,6 +1074,12 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedAttnParam
     const auto row_of = [&](int k) { return ((size_t)k * 2 + (k == c)) * kRows + r; };
     float M = sg;
     float4 ml = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+    // O of the first parts beside the statistics, not after them
+    constexpr int kAhead = 4;
+    float4 ahead[kAhead];
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e)
+      if (c + e <= last) ahead[e] = reinterpret_cast<const float4*>(p.ws_o + row_of(c + e) * 128)[lane];
     for (int k0 = c; k0 <= last; k0 += 32) {
       if (k0 + lane <= last) {
         ml = p.ws_ml[row_of(k0 + lane)];
@@ -1092,15 +1098,22 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedAttnParam
         const float w = (ml.x == -INFINITY) ? 0.f : ex2(ml.x - M);
         Z += w * ml.y;
         Zr += w * ml.z;
-#pragma unroll 4
-        for (int e = 0; e < parts; ++e) {
+        const auto add = [&](int e, const float4& o) {
           const float we = __shfl_sync(0xffffffffu, w, e);
-          const float4 o = reinterpret_cast<const float4*>(p.ws_o + row_of(k0 + e) * 128)[lane];
           acc.x += we * o.x;
           acc.y += we * o.y;
           acc.z += we * o.z;
           acc.w += we * o.w;
+        };
+        int e0 = 0;
+        if (k0 == c) {
+#pragma unroll
+          for (int e = 0; e < kAhead; ++e)
+            if (e < parts) add(e, ahead[e]);
+          e0 = kAhead;
         }
+#pragma unroll 4
+        for (int e = e0; e < parts; ++e) add(e, reinterpret_cast<const float4*>(p.ws_o + row_of(k0 + e) * 128)[lane]);
       }
 #pragma unroll
       for (int e = 16; e > 0; e >>= 1) {

@@ -40,8 +40,8 @@ constexpr int kPdKeys = 64;
 constexpr int kPdStages = 2;
 constexpr int kPdBox = kPdKeys * 128;           // [keys][64 dims]
 constexpr int kPdStageBytes = 5 * kPdBox;       // K: 3 boxes, V: 2 boxes
-constexpr int kPdQRow = 400;                    // 384 B + 16: ldmatrix rows on distinct banks
-constexpr int kPdQBytes = kPdRows * kPdQRow;
+constexpr int kPdQBox = kPdRows * 128;          // [heads][64 dims]
+constexpr int kPdQBytes = 3 * kPdQBox;
 constexpr int kPdORow = 136;                    // padded row of the merge buffers
 constexpr int kPdOffQ = kPdStages * kPdStageBytes;          // 2 buffers
 constexpr int kPdOffO = kPdOffQ + 2 * kPdQBytes;            // 2 x [16][kPdORow] fp32
@@ -51,8 +51,8 @@ constexpr int kPdSmemBytes = kPdOffBar + 256 + 1024;  // barriers, plan; alignme
 static_assert(2 * (kPdSmemBytes + 1024) <= 228 * 1024, "two CTAs to an SM");
 
 __global__ void __launch_bounds__(kPdThreads, 2)
-    paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                        const __grid_constant__ PagedAttnParams p) {
+    paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedAttnParams p) {
   extern __shared__ __align__(1024) uint8_t pdsmem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(pdsmem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kPdOffBar);
@@ -72,6 +72,7 @@ __global__ void __launch_bounds__(kPdThreads, 2)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 128) {
+    tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
     for (int s = 0; s < 2; ++s) {
@@ -112,11 +113,11 @@ __global__ void __launch_bounds__(kPdThreads, 2)
       look_up();
       const int qb = n & 1;
       if (n >= 2 && !(ok = wait_warp(&q_empty[qb], ((n >> 1) - 1) & 1, abort_flag))) break;
-      if (lane == 0) mbar_arrive_expect_tx(&q_full[qb], p.G * 384);
-      __syncwarp();
-      if (lane < p.G) {
-        const size_t at = (size_t)it.tok0 * p.Hq + it.g * p.G + lane;
-        bulk_load(smem + kPdOffQ + qb * kPdQBytes + lane * kPdQRow, p.q + at * 192, 384, &q_full[qb]);
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&q_full[qb], p.G * 384);
+#pragma unroll
+        for (int c = 0; c < 3; ++c)
+          tma_load_3d(smem + kPdOffQ + qb * kPdQBytes + c * kPdQBox, &tm_q, &q_full[qb], c * 64, it.g * p.G, it.tok0);
       }
       ++n;
       while (k0 < end) {
@@ -155,13 +156,16 @@ __global__ void __launch_bounds__(kPdThreads, 2)
   while (ok && walk.next(p, it)) {
     const int rows = p.G;
     const int qb = n & 1;
+    // the sink of the row that this thread writes: here, a load off the item's end
+    const int row = threadIdx.x >> 3;
+    const float sg = p.sinks && row < rows ? p.sinks[it.g * p.G + row] * 1.4426950408889634f : -INFINITY;
     uint32_t qa[12][4];
     if ((ok = wait_bounded(&q_full[qb], (n >> 1) & 1, abort_flag))) {
       // fragments of all 12 k-steps of 16 dims; rows that hold nothing are zero
-      const uint32_t qrow = sbase + kPdOffQ + qb * kPdQBytes + (lane & 15) * kPdQRow + (lane >> 4) * 16;
+      const uint32_t qs = sbase + kPdOffQ + qb * kPdQBytes;
 #pragma unroll
       for (int kk = 0; kk < 12; ++kk) {
-        ldsm_x4(qrow + kk * 32, qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3]);
+        ldsm_x4(qs + (kk >> 2) * kPdQBox + sw128_offset(lane & 15, (kk & 3) * 16 + (lane >> 4) * 8), qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3]);
         if (r0 >= rows) qa[kk][0] = qa[kk][2] = 0u;
         if (r0 + 8 >= rows) qa[kk][1] = qa[kk][3] = 0u;
       }
@@ -318,7 +322,7 @@ __global__ void __launch_bounds__(kPdThreads, 2)
     // every warp comes to the same decision: the flags change only two items on
     ok = fine[(n & 1) * 4] && fine[(n & 1) * 4 + 1] && fine[(n & 1) * 4 + 2] && fine[(n & 1) * 4 + 3];
     // ---- 128 threads: row tid / 8, columns 4 (tid & 7) + 32 j
-    const int tid = threadIdx.x, row = tid >> 3, cb = (tid & 7) * 4;
+    const int tid = threadIdx.x, cb = (tid & 7) * 4;
     float M = -INFINITY;
 #pragma unroll
     for (int w = 0; w < 4; ++w) M = fmaxf(M, sm[w * kPdRows + row]);
@@ -359,7 +363,6 @@ __global__ void __launch_bounds__(kPdThreads, 2)
         }
       } else if (MIMO_ROW_OK((long long)tok * p.Hq + h, (long long)p.pb.total_q * p.Hq)) {
         // fold the sink: it joins the normaliser only
-        const float sg = p.sinks ? p.sinks[h] * 1.4426950408889634f : -INFINITY;
         const float Mf = fmaxf(M, sg);
         const float scl = M == -INFINITY ? 0.f : ex2(M - Mf), ps = sg == -INFINITY ? 0.f : ex2(sg - Mf);
         const float Lf = L * scl + ps, Lrf = Lr * scl + ps;

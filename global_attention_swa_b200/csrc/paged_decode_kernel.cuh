@@ -189,6 +189,7 @@ __global__ void __launch_bounds__(kPdThreads, 2)
         // ---- S = Q K^T for 16 keys (two n-blocks of 8).  ldmatrix.x4 rows: lanes 0-7
         // keys 0..7 dims +0; 8-15 the same dims +8; 16-31 keys 8..15.
         float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        float s1[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};  // odd steps: two shorter chains
         {
           const int krow = kw + (lane & 7) + ((lane >> 4) << 3);
           const int kcol = ((lane >> 3) & 1) * 8;
@@ -196,9 +197,11 @@ __global__ void __launch_bounds__(kPdThreads, 2)
           for (int kk = 0; kk < 12; ++kk) {
             uint32_t b0, b1, b2, b3;
             ldsm_x4(kb + (kk >> 2) * kPdBox + sw128_offset(krow, (kk & 3) * 16 + kcol), b0, b1, b2, b3);
-            mma_bf16_16816(s[0], qa[kk], b0, b1);
-            mma_bf16_16816(s[1], qa[kk], b2, b3);
+            mma_bf16_16816(kk & 1 ? s1[0] : s[0], qa[kk], b0, b1);
+            mma_bf16_16816(kk & 1 ? s1[1] : s[1], qa[kk], b2, b3);
           }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) s[e >> 2][e & 3] += s1[e >> 2][e & 3];
         }
         // ---- scale to base 2, mask, running max
         float mx0 = -INFINITY, mx1 = -INFINITY;

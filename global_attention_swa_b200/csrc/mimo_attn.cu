@@ -930,11 +930,11 @@ mimo::PagedBatch paged_batch(const int32_t* block_table, const int32_t* cu_seqle
 // Which kernel a call over a paged cache takes, by the most new tokens a
 // sequence brings and the G query heads of a key/value head.
 //   decode  one token, G <= 16: warp-level MMAs, two CTAs to an SM (64 sequences
-//           of 1024 to 32768 keys 528 us, by tiles 536; window 129 13 and 21)
+//           of 1024 to 32768 keys 527 us, by tiles 536; window 129 12 and 21)
 //   window  all keys of one or two blocks of 128 / G tokens fit a score tile
 //           (window 129, 5600 tokens: 72 us, by tiles 159; one block 79)
 //   tile    one tile of 128 / G tokens, or two that share their key tiles (1 to 6
-//           tokens at up to 16384 keys: 134 and 171 us; 2048 at 32768: 2.43 and
+//           tokens at up to 16384 keys: 133 and 171 us; 2048 at 32768: 2.43 and
 //           2.28 ms)
 struct PagedVariant {
   enum Kind { decode, window, tile } kind;

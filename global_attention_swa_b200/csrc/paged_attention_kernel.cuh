@@ -39,7 +39,8 @@
 //
 // Bounds, measured on one B200 (64 query heads, 4 key/value heads):
 //   one tile   the cache's bytes: 32 sequences of up to 16384 keys and 1 to 6 new
-//              tokens, 697 MB in 134 us, 5.2 TB/s (79 % of a plain copy's rate).
+//              tokens, 697 MB in 133 us, 5.2 TB/s (80 % of a plain copy's rate).
+//              CTAs of equal shares end between 109 and 127 us.
 //   two tiles  the products and, beside them, the exponentials: 2048 tokens at
 //              length 32768, 2.66 TFLOP in 2.28 ms, 1170 TFLOP/s (70 % of a large
 //              bf16 GEMM's burst rate; 2.5 ms, 75 % of its sustained rate, where
@@ -65,7 +66,7 @@ constexpr int kPgKStages = 2;
 // Two tiles share a key tile: Q 2 x 48 KB, K 2 x 48 KB, V 32 KB.  One tile (a
 // handful of new tokens: bound by the cache's bytes): V has two stages too.
 // Each is the faster one on its side: 2048 new tokens 2.28 ms with two tiles,
-// 2.43 with one; 1 to 6 new tokens 134 us with one, 171 with two.
+// 2.43 with one; 1 to 6 new tokens 133 us with one, 171 with two.
 template <int kTiles>
 struct PgLayout {
   static constexpr int kVStages = kTiles == 1 ? 2 : 1;
@@ -115,12 +116,13 @@ struct PgPlace {
 };
 
 // Cost of an item of a sequence, in keys: what it reads, and kPgItemCost for
-// its queries, its latencies and its epilogue (about what two key tiles take).
+// its queries, its latencies and its epilogue (a fit over the CTAs of a batch of
+// drafts: 1.6 us a key tile, 4.7 an item).
 // In a window that is the same for all blocks; without one, block i reads
 // first + D (i + 1) keys (first: the position of the chunk's first token, D:
-// tokens of a block).  With whole items only, 1.  (Without that cost: drafts 142
-// against 134 us, three short chats 19.6 against 17.8; with twice of it 135 and 18.2.)
-constexpr int kPgItemCost = 2 * kPgKeys;
+// tokens of a block).  With whole items only, 1.  (Those drafts take 133 us with
+// a cost of three key tiles, 134 with two, 135 with four, 142 without.)
+constexpr int kPgItemCost = 3 * kPgKeys;
 // Quotient of non-negative values; nearly always both fit 32 bits, and a 64-bit
 // division is a long chain of dependent instructions.
 __device__ __forceinline__ long long pg_div(long long a, long long b) {
@@ -414,8 +416,8 @@ __device__ __forceinline__ bool pg_plan(const PagedAttnParams& p, PgPlace* plan,
     total += x;
   }
   before += incl - mine;
-  // no share below a key tile: three chats of up to 700 keys take 16.4 us so, 17.8
-  // with at least two tiles to a share, 21.8 with four
+  // no share below a key tile: with at least two tiles to a share three chats of up
+  // to 700 keys take 1.4 us more (of 15), with four 5.4
   const long long unit = p.split ? kPgKeys : 1;
   const long long shares = max(1LL, min((long long)gridDim.x, pg_div(total, unit)));
   const int c = blockIdx.x;

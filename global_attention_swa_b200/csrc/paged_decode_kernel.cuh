@@ -17,11 +17,11 @@
 //               P V in registers; joined at an item's end
 //
 // Measured on one B200 (64 query heads, 4 key/value heads): 64 sequences of 1024
-// to 32768 keys, 3.27 GB in 528 us, 6.2 TB/s, 95 % of a plain copy's rate; under
-// a window of 129, 23.8 MB in 13 us, where latency binds: the share is found, the
-// page looked up, K and V fetched and the warps joined once, one after the other.
-// The general kernel takes 536 and 21 to 24 us; three sequences of up to 700 keys
-// 17.8 here and 18.8 there.
+// to 32768 keys, 3.27 GB in 514 to 527 us, 6.3 TB/s, 95 to 97 % of a plain copy's
+// rate; under a window of 129, 23.8 MB in 12 us, where latency binds: the share is
+// found (2 us), its pages and loads (2), three tiles (3), the join (2), one after the
+// other.  The general kernel takes 536 and 21 to 24 us; three sequences of up to
+// 700 keys 15.3 here, 1 us more there.
 //
 // P is rounded to bf16 for the P V product (bf16 V) and the output normalised
 // by the sum of the rounded values; everything else is fp32.

@@ -13,15 +13,16 @@
 // next one's scores are computed and the queries of the one after are on their way.
 //
 // Measured on one B200 (64 query heads, 4 key/value heads, window 129, 5600 new
-// tokens of 9 sequences, 229 MB): 72 us, 3.2 TB/s, 49 % of a plain copy's rate
-// (the general kernel: 159 us; one block to an item: 79 us).  Bound by the chain
+// tokens of 9 sequences, 229 MB): 69.5 us, 3.3 TB/s, 50 % of a plain copy's rate
+// (the general kernel: 159 us; one block to an item, at 72 for two: 79 us).  Bound by the chain
 // of one block, scores, softmax, P V, store, of which two are under way at once:
 // TMEM holds two score tiles of 160 columns and one O.
 //
 //   warp 12     loads Q (two buffers, a block ahead) and K (once per item, a
 //               lane per box of 16 keys; the page table is looked up here)
 //   warp 13     MMA issuer: S(n) = Q K^T into score buffer n & 1, then O = P(n-1) V
-//   warp 14     loads V (once per item, as K) and zeroes its rows that nothing sees
+//   warp 14     loads V (once per item, as K) and zeroes its rows past the
+//               sequence's end
 //   warp 15     works out the items of this CTA's share, ahead of the others
 //   warps 0-7   softmax: warpgroup s takes the blocks with n & 1 == s, one row
 //               per thread, one pass over its TMEM row
@@ -60,6 +61,13 @@ static_assert(kPwOffOnes % 1024 == 0 && kPwColSum + 16 <= 512 && kPwSmemBytes <=
 
 // An item's keys, all in one tile.
 __device__ __forceinline__ PgTile pw_keys(const PgItem& it) { return pg_keys(it, it.start, kPwKeys); }
+
+// Its last rows lie past the sequence's end: their slots may hold anything, and are
+// zeroed before the product.  Other rows that nothing sees hold values of the same
+// sequence and stay: what is not finite among them is met as in any hidden key
+// (pw_row_again), and V goes to its products without a warp between (with an
+// item fetched ahead by the issuer, 69.5 against 72.5 us).
+__device__ __forceinline__ bool pw_open(const PgItem& it, const PgTile& keys) { return keys.k0 + keys.n > it.len; }
 
 // One row (packed row tok, head h, position pos) from the definition, its output
 // only: keys that it does not see take no part at all.  For rows whose product
@@ -262,10 +270,14 @@ __global__ void __launch_bounds__(kPwThreads, 1)
       const uint32_t dV = desc_lo_sw128(sbase + kPwOffV, kPwKBox);
       bool ok = true;
       // O = P(m) V over k keys: 16 to an MMA (P: 8 TMEM columns; V: 16 rows = 2 KB)
-      const auto do_pv = [&](int m, int item, int k, bool first_of_item, bool last_of_item) {
+      int opened = 0;  // items whose V was zeroed in part: phases of v_ready
+      const auto do_pv = [&](int m, int item, int k, bool first_of_item, bool last_of_item, bool open) {
         const int bm = m & 1;
         if (!(ok = wait_bounded(&p_full[bm], (m >> 1) & 1, abort_flag))) return;
-        if (first_of_item && !(ok = wait_bounded(v_ready, item & 1, abort_flag))) return;
+        if (first_of_item) {
+          if (!(ok = wait_bounded(v_full, item & 1, abort_flag))) return;
+          if (open && !(ok = wait_bounded(v_ready, opened++ & 1, abort_flag))) return;
+        }
         if (m >= 1 && !(ok = wait_bounded(o_empty, (m - 1) & 1, abort_flag))) return;
         tc_fence_after();
         const uint32_t tP = tbase + bm * kPwKeys;
@@ -277,9 +289,13 @@ __global__ void __launch_bounds__(kPwThreads, 1)
       };
       int n = 0, kp = 0;
       int pm = -1, pkp = 0, pk = 0;  // previous block: number, item, keys
-      bool pfirst = false, plast = false;
-      while (ok && next(false)) {
-        const int nblk = blocks_of(it), k = pw_keys(it).n;
+      bool pfirst = false, plast = false, popen = false;
+      bool have = next(false);
+      while (ok && have) {
+        const int nblk = blocks_of(it);
+        const PgTile keys = pw_keys(it);
+        const int k = keys.n;
+        const bool open = pw_open(it, keys);
         const uint32_t idesc_s = idesc_bf16_f32(128, 0, false, false) | (static_cast<uint32_t>(k >> 3) << 17);
         for (int blk = 0; ok && blk < nblk; ++blk, ++n) {
           const int b = n & 1;
@@ -295,17 +311,21 @@ __global__ void __launch_bounds__(kPwThreads, 1)
           }
           umma_commit(&s_full[b]);
           umma_commit(&q_empty[b]);
-          if (blk == nblk - 1) umma_commit(k_empty);
-          if (pm >= 0) do_pv(pm, pkp, pk, pfirst, plast);
+          if (blk == nblk - 1) {
+            umma_commit(k_empty);
+            have = next(false);  // here, where the thread would wait for P
+          }
+          if (pm >= 0) do_pv(pm, pkp, pk, pfirst, plast, popen);
           pm = n;
           pkp = kp;
           pk = k;
           pfirst = blk == 0;
           plast = blk == nblk - 1;
+          popen = open;
         }
         ++kp;
       }
-      if (ok && pm >= 0) do_pv(pm, pkp, pk, pfirst, plast);
+      if (ok && pm >= 0) do_pv(pm, pkp, pk, pfirst, plast, popen);
     }
   } else if (warp == 14) {
     // ------------------------------------------------------------ V, and its rows nothing sees
@@ -324,16 +344,14 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         for (int c = 0; c < 2; ++c)
           tma_load_3d(smem + kPwOffV + c * kPwKBox + lane * kPwBoxRows * 128, &tm_v, v_full, c * 64, it.g, row);
       }
-      if (!wait_warp(v_full, kp & 1, abort_flag)) break;
-      if (keys.zlo > 0 || keys.zhi < keys.n) {
+      if (pw_open(it, keys)) {
+        if (!wait_warp(v_full, kp & 1, abort_flag)) break;
         pg_zero_unseen(keys, sbase + kPwOffV, kPwKBox);
         fence_proxy_async_smem();
         __syncwarp();
+        if (lane == 0) mbar_arrive(v_ready);
       }
-      if (lane == 0) {
-        mbar_arrive(v_ready);
-        mbar_arrive(&i_empty[kp % kPgItems]);
-      }
+      if (lane == 0) mbar_arrive(&i_empty[kp % kPgItems]);
       ++kp;
     }
   } else if (warp == 15) {

@@ -21,8 +21,8 @@
 //   warp 12     loads Q (two buffers, a block ahead) and K (once per item, a
 //               lane per box of 16 keys; the page table is looked up here)
 //   warp 13     MMA issuer: S(n) = Q K^T into score buffer n & 1, then O = P(n-1) V
-//   warp 14     loads V (once per item, as K) and zeroes its rows past the
-//               sequence's end
+//   warp 14     loads V (once per item, as K) and zeroes rows of it that
+//               may never have been written
 //   warp 15     works out the items of this CTA's share, ahead of the others
 //   warps 0-7   softmax: warpgroup s takes the blocks with n & 1 == s, one row
 //               per thread, one pass over its TMEM row
@@ -62,12 +62,15 @@ static_assert(kPwOffOnes % 1024 == 0 && kPwColSum + 16 <= 512 && kPwSmemBytes <=
 // An item's keys, all in one tile.
 __device__ __forceinline__ PgTile pw_keys(const PgItem& it) { return pg_keys(it, it.start, kPwKeys); }
 
-// Its last rows lie past the sequence's end: their slots may hold anything, and are
-// zeroed before the product.  Other rows that nothing sees hold values of the same
-// sequence and stay: what is not finite among them is met as in any hidden key
-// (pw_row_again), and V goes to its products without a warp between (with an
-// item fetched ahead by the issuer, 69.5 against 72.5 us).
-__device__ __forceinline__ bool pw_open(const PgItem& it, const PgTile& keys) { return keys.k0 + keys.n > it.len; }
+// Rows past the sequence's end, and before the first key that its chunk sees, may
+// never have been written: they are zeroed before the product.  Other rows that
+// nothing of the item sees are, nearly all, seen by another item, and stay: what is
+// not finite among them is met as in any hidden key (pw_row_again), and V goes to its
+// products without a warp between (with an item fetched ahead by the issuer, 69.5
+// against 72.5 us).
+__device__ __forceinline__ bool pw_open(const PgItem& it, const PgTile& keys) {
+  return it.outer && (keys.zlo > 0 || keys.zhi < keys.n);
+}
 
 // One row (packed row tok, head h, position pos) from the definition, its output
 // only: keys that it does not see take no part at all.  For rows whose product

@@ -185,7 +185,7 @@ struct PgItem {
   int t0, t1;       // the tiles of this share
   int turn;         // the order of their passage: from t0 + turn on, then from t0
   int n_last;       // keys that the products take of the last tile, a multiple of 16
-  int e0, e1;       // tiles below e0 and from e1 on are edges (PgTile::edge)
+  int e0, e1;       // tiles below e0 and from e1 on hold values that some row must not meet
   __device__ __forceinline__ int count() const { return t1 - t0; }
   __device__ __forceinline__ int width(int t) const { return t == n_kt - 1 ? n_last : kPgKeys; }
   __device__ __forceinline__ bool edge(int t) const { return t < e0 || t >= e1; }
@@ -273,8 +273,6 @@ struct PgWalk {
 // and [hi, hi_end) by some rows only.
 struct PgTile {
   int k0, n, zlo, zhi, lo, lo_end, hi, hi_end;
-  // Its values are looked through before the product.
-  __device__ __forceinline__ bool edge() const { return zlo > 0 || zhi < n || lo_end > lo || hi_end > hi; }
 };
 __device__ __forceinline__ PgTile pg_keys(const PgItem& it, int k0, int most) {
   PgTile r;

@@ -14,9 +14,10 @@
 //
 // Measured on one B200 (64 query heads, 4 key/value heads, window 129, 5600 new
 // tokens of 9 sequences, 229 MB): 69.5 us, 3.3 TB/s, 50 % of a plain copy's rate
-// (the general kernel: 159 us; one block to an item, at 72 for two: 79 us).  Bound by the chain
-// of one block, scores, softmax, P V, store, of which two are under way at once:
-// TMEM holds two score tiles of 160 columns and one O.
+// (the general kernel: 159 us; one block to an item, at 72 for two: 79 us).  Bound
+// by the chain of one block, scores (0.8 us), softmax (2.2), P V (0.6), of which
+// two are under way at once: P lies over its scores, and TMEM holds two score tiles
+// of 160 columns beside O.
 //
 //   warp 12     loads Q (two buffers, a block ahead) and K (once per item, a
 //               lane per box of 16 keys; the page table is looked up here)

@@ -50,6 +50,7 @@ class PagedCache:
         self._spare_table = torch.empty_like(self.block_table)
         self.seqlens = torch.zeros(num_seqs, **ints)
         self.info = torch.zeros(2, **ints)
+        self._attend = torch.zeros(num_seqs, **ints)  # what attend goes by: -1 where extend found no room
         self._kept = torch.zeros(num_seqs, **ints)  # first position whose page was never released
         self.page_size, self.window, self.rollback = page_size, window, rollback
         self.capacity = max_pages * page_size
@@ -73,12 +74,14 @@ class PagedCache:
         is replaced by a copy, in every layer.  If the pool does not have the pages,
         nothing changes and ``info[0]`` says how many were missing; a sequence that
         would pass max_pages pages stays as it is and is recorded as an invalid
-        argument in the device status.  Returns ``info``."""
+        argument in the device status.  ``attend`` skips sequences that were not
+        extended, and records that too.  Returns ``info``."""
         lens = self.seqlens + new_tokens
         first = self._first()
         moves = self._hold(lens, first, self.seqlens)
         mimo.mimo_attn_page_copy(self.k_pages, self.v_pages, moves)
         done = (self.info[0] == 0) & (lens >= 0) & (lens <= self.capacity)
+        self._attend.copy_(torch.where(done, lens, -1))
         self.seqlens.copy_(torch.where(done, lens, self.seqlens))
         if first is not None:
             self._kept.copy_(torch.where(done, first, self._kept))
@@ -90,11 +93,11 @@ class PagedCache:
         rotated (rope_theta None: they already are), k and v written, and q attends over
         the cache.  Rows are packed by cu_seqlens_q.  Returns (out [Nt,Hq,128], lse [Hq,Nt])."""
         kp, vp = self.k_pages[layer], self.v_pages[layer]
-        q = mimo.mimo_attn_paged_append(q, k, v, kp, vp, self.block_table, cu_seqlens_q, self.seqlens,
+        q = mimo.mimo_attn_paged_append(q, k, v, kp, vp, self.block_table, cu_seqlens_q, self._attend,
                                         1.0 if rope_theta is None else rope_theta,
                                         0 if rope_theta is None else rotary_dim,
                                         q_out=q if rope_theta is None else None)
-        return mimo.mimo_attn_paged_attention(q, kp, vp, self.block_table, cu_seqlens_q, self.seqlens,
+        return mimo.mimo_attn_paged_attention(q, kp, vp, self.block_table, cu_seqlens_q, self._attend,
                                               max_seqlen_q, self.window, sinks, out_dtype=out_dtype,
                                               softmax_scale=softmax_scale, v_scale=v_scale)
 
@@ -106,6 +109,7 @@ class PagedCache:
         # what extend kept stays, so that a later call may go back further
         self._hold(lens, self._kept if self.window else None, None)
         self.seqlens.copy_(torch.where(lens >= 0, lens, self.seqlens))  # a negative one was recorded
+        self._attend.copy_(self.seqlens)
         self._kept.mul_(lens != 0)
         return self.info
 
@@ -120,6 +124,7 @@ class PagedCache:
         source, real = parent.clamp(0, slots - 1).long(), (parent >= 0) & (parent < slots)
         for t in (self.seqlens, self._kept):
             t.copy_(t[source] * real)
+        self._attend.copy_(self.seqlens)
 
     def compact(self, max_moves):
         """Move used pages from the end of the pools to free places at their front, at most

@@ -362,7 +362,7 @@ size_t mimo_attn_paged_attention_workspace_size(const mimo_attn_dims_t* dims, in
  * window > 0.
  *
  *   q            [total_q, Hq, Dqk] bf16, post-RoPE
- *   max_seqlen_q >= every n_b (not read back from the device)
+ *   max_seqlen_q >= every n_b (not read back from the device), <= total_q
  *   window       0 = global; >= 1 = the query plus window-1 earlier keys
  *   sinks        [Hq] fp32 or NULL
  *   out          [total_q, Hq, Dv] in dims->out_dtype

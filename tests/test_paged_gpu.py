@@ -702,6 +702,45 @@ def test_the_cache_keeps_its_sequences_through_bad_requests():
         assert held == [-(-n // 16) for n in lens] and int(cache.page_refs.sum()) == sum(held)
 
 
+def test_attend_after_an_extend_without_room_writes_nothing():
+    """Neither where the pool lacks pages nor in the sequence that would pass its table: the
+    keys and values that are there stay, the rows of the output too, and it is recorded."""
+    g = torch.Generator().manual_seed(3)
+
+    def chunk(n):
+        return [torch.randn((n, h, d), generator=g).to(torch.bfloat16).cuda() for h, d in ((8, 192), (2, 192), (2, 128))]
+
+    for pool, news, skipped in ((6, [30, 30], [0, 1]), (40, [30, 50], [1])):
+        cache = PagedCache(1, pool, 16, 2, 5, 2)
+        cu = ints([0, 40, 80]).cuda()
+        cache.extend(ints([40, 40]).cuda())
+        cache.attend(0, *chunk(80), cu, 40, None, 1e4)
+        mimo.mimo_attn_device_status()
+        k, v = cache.k_pages.clone(), cache.v_pages.clone()
+        cache.extend(ints(news).cuda())
+        cu = ints([0, news[0], sum(news)]).cuda()
+        try:
+            mimo.mimo_attn_device_status()
+            assert skipped == [0, 1]
+        except mimo.MimoAttnError:
+            assert skipped == [1]
+        cache.attend(0, *chunk(sum(news)), cu, max(news), None, 1e4)
+        with pytest.raises(mimo.MimoAttnError) as e:
+            mimo.mimo_attn_device_status()
+        assert e.value.status == mimo.MIMO_ERR_INVALID_ARG
+        for b in skipped:
+            assert cache.seqlens[b] == 40
+            held = cache.block_table[b, :3].long()
+            assert torch.equal(cache.k_pages[0, held], k[0, held]) and torch.equal(cache.v_pages[0, held], v[0, held])
+        # the next step goes on
+        cache.extend(ints([0, 1] if skipped == [1] else [8, 8]).cuda())
+        n = 1 if skipped == [1] else 16
+        cu = ints([0, 0, 1] if skipped == [1] else [0, 8, 16]).cuda()
+        out, _ = cache.attend(0, *chunk(n), cu, min(n, 8), None, 1e4)
+        mimo.mimo_attn_device_status()
+        assert torch.isfinite(out).all()
+
+
 def test_a_windowed_cache_goes_back_more_than_once():
     """Down to the length before the last extend (less the rollback), in steps: what the
     queries from there on see is still held, in the same pages."""

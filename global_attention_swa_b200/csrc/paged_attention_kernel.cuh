@@ -379,10 +379,14 @@ __device__ __forceinline__ void pg_schedule(const PagedAttnParams& p, const PgPl
   }
 }
 // Item n is there to read; false past the last one, or after a timed-out wait.
-// Each reader arrives once on empty[n % kPgItems] when it is done with it.
+// Each reader arrives once on empty[n % kPgItems] when it is done with it.  kWarp:
+// the reader is a whole warp, not one thread.
+template <bool kWarp>
 __device__ __forceinline__ bool pg_item(const PgQueue& q, uint64_t* full, int n, volatile int* abort) {
   const int s = n % kPgItems;
-  return wait_bounded(&full[s], (n / kPgItems) & 1, abort) && *const_cast<const volatile int*>(&q.more[s]);
+  const uint32_t parity = (n / kPgItems) & 1;
+  return (kWarp ? wait_lanes(&full[s], parity, abort) : wait_bounded(&full[s], parity, abort)) &&
+         *const_cast<const volatile int*>(&q.more[s]);
 }
 
 // This CTA's share.  All threads call it; plan (shared) holds the first place
@@ -588,7 +592,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     if (work) {
       int n = 0, kt = 0;  // items and key tiles loaded
       bool ok = true;
-      while (ok && pg_item(queue, i_full, n, abort_flag)) {
+      while (ok && pg_item<true>(queue, i_full, n, abort_flag)) {
         const PgItem it = queue.it[n % kPgItems];
         __syncwarp();
         if (lane == 0) mbar_arrive(&i_empty[n % kPgItems]);
@@ -631,7 +635,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     if (work) {
       int kt = 0;
       bool ok = true;
-      for (int n = 0; ok && pg_item(queue, i_full, n, abort_flag); ++n) {
+      for (int n = 0; ok && pg_item<true>(queue, i_full, n, abort_flag); ++n) {
         const PgItem it = queue.it[n % kPgItems];
         for (int j = 0; j < it.count(); ++j, ++kt) {
           const PgTile tl = pg_tile(it, it.tile(j));
@@ -708,7 +712,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         edges ^= 1u << vs;
         return wait_bounded(&v_ready[vs], ~(edges >> vs) & 1, abort_flag);
       };
-      while (ok && pg_item(queue, i_full, n, abort_flag)) {
+      while (ok && pg_item<false>(queue, i_full, n, abort_flag)) {
         const PgItem it = queue.it[n % kPgItems];
         mbar_arrive(&i_empty[n % kPgItems]);
         const bool has1 = kTiles == 2 && it.tokens > p.TQ;
@@ -805,7 +809,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     int tg = 0;  // score tiles it consumed
     bool ok = true;
     // The item stays in shared memory: the loop over key tiles needs every register.
-    for (int item = 0; ok && work && (kTiles == 2 || i == 0) && pg_item(queue, i_full, item, abort_flag); ++item) {
+    for (int item = 0; ok && work && (kTiles == 2 || i == 0) && pg_item<true>(queue, i_full, item, abort_flag); ++item) {
       const PgItem& it = queue.it[item % kPgItems];
       const auto done = [&]() {
         __syncwarp();
@@ -845,7 +849,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         const int buf = kTiles == 1 ? (tg & 1) : i;
         const int phase = kTiles == 1 ? (tg >> 1) & 1 : tg & 1;
         const uint32_t tS = tbase + lane_off + buf * 128;
-        if (!(ok = wait_bounded(&s_full[buf], phase, abort_flag))) break;
+        if (!(ok = wait_lanes(&s_full[buf], phase, abort_flag))) break;
         tc_fence_after();
         if (warp_ok) {
           float s[128];
@@ -884,7 +888,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
               // committed after it, with one it may still run
               if (kTiles == 1) {
                 const int prev = tg - 1;
-                wait_bounded(&v_empty[prev % kVStages], (prev / kVStages) & 1, abort_flag);
+                wait_lanes(&v_empty[prev % kVStages], (prev / kVStages) & 1, abort_flag);
                 tc_fence_after();
               }
 #pragma unroll 1
@@ -943,7 +947,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       if (!ok) break;
       // ---------------- epilogue: O is read out of TMEM first and released, so
       // the next item's P.V can start at once.
-      if (!(ok = wait_bounded(&o_full[i], n & 1, abort_flag))) break;
+      if (!(ok = wait_lanes(&o_full[i], n & 1, abort_flag))) break;
       tc_fence_after();
       float o[128];
       tmem_load128_sync(tO, o);

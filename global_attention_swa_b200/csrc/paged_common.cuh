@@ -48,6 +48,14 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volati
   return __shfl_sync(0xffffffffu, ok, 0);
 }
 
+// wait_bounded for a whole warp, polled by every lane, with one answer for all of
+// them.  Lanes leave the poll one by one, and where time runs out some may have seen
+// the phase and others not; what follows such a wait is done by the whole warp at
+// once (TMEM accesses, ldmatrix, votes), and needs every lane there.
+__device__ __forceinline__ bool wait_lanes(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort));
+}
+
 // The sequence of packed row t, found by the whole warp: how many sequences
 // end at or before t (32 of cu_q at a time, 32 runs of it first); -1 for a row
 // that none owns.  For a sound cu_q that is the sequence with cu_q[b] <= t <

@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kPdThreads, 2)
     const int row = threadIdx.x >> 3;
     const float sg = p.sinks && row < rows ? p.sinks[it.g * p.G + row] * 1.4426950408889634f : -INFINITY;
     uint32_t qa[12][4];
-    if ((ok = wait_bounded(&q_full[qb], (n >> 1) & 1, abort_flag))) {
+    if ((ok = wait_lanes(&q_full[qb], (n >> 1) & 1, abort_flag))) {
       // fragments of all 12 k-steps of 16 dims; rows that hold nothing are zero
       const uint32_t qs = sbase + kPdOffQ + qb * kPdQBytes;
 #pragma unroll
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kPdThreads, 2)
     const int end = min(it.hi + 1, it.start + it.t1 * kPgKeys);
     for (int k0 = it.start + it.t0 * kPgKeys; ok && k0 < end; k0 += kPdKeys, ++kt) {
       const int st = kt & 1;
-      if (!(ok = wait_bounded(&full[st], (kt >> 1) & 1, abort_flag))) break;
+      if (!(ok = wait_lanes(&full[st], (kt >> 1) & 1, abort_flag))) break;
       const int kpos = k0 + kw;  // this warp's first key
       if (kpos < end && kpos + 15 >= it.lo) {
         const uint32_t kb = sbase + st * kPdStageBytes;

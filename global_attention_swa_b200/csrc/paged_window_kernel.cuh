@@ -202,7 +202,8 @@ __global__ void __launch_bounds__(kPwThreads, 1)
   int items = 0;  // taken by this role
   PgItem it;
   const auto next = [&](bool warp_wide) {  // the item is copied and released at once
-    if (!pg_item(queue, i_full, items, abort_flag)) return false;
+    if (!(warp_wide ? pg_item<true>(queue, i_full, items, abort_flag) : pg_item<false>(queue, i_full, items, abort_flag)))
+      return false;
     it = queue.it[items % kPgItems];
     if (warp_wide) __syncwarp();
     if (!warp_wide || lane == 0) mbar_arrive(&i_empty[items % kPgItems]);
@@ -334,7 +335,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
   } else if (warp == 14) {
     // ------------------------------------------------------------ V, and its rows nothing sees
     int kp = 0;
-    while (pg_item(queue, i_full, kp, abort_flag)) {
+    while (pg_item<true>(queue, i_full, kp, abort_flag)) {
       const PgItem it = queue.it[kp % kPgItems];
       const PgTile keys = pw_keys(it);
       const int boxes = keys.n / kPwBoxRows;
@@ -383,7 +384,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         const int c_hi = qpos - keys.k0;                              // keys <= qpos
         const int c_lo = max(qpos - p.window + 1, 0) - keys.k0;       // keys in window, >= 0
         const float sg2 = p.sinks && a < tokens ? p.sinks[hg] * 1.4426950408889634f : -INFINITY;
-        if (!(ok = wait_bounded(&s_full[b], (n >> 1) & 1, abort_flag))) break;
+        if (!(ok = wait_lanes(&s_full[b], (n >> 1) & 1, abort_flag))) break;
         tc_fence_after();
         const uint32_t tS = tbase + lane_off + b * kPwKeys;
         float m = sg2, l = 0.f;
@@ -453,7 +454,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         tc_fence_before();
         mbar_arrive(&p_full[b]);
         const float ps = (sg2 != -INFINITY) ? ex2(sg2 - m) : 0.f;  // the sink's term
-        if (n >= 2 && !(ok = wait_bounded(&ml_empty[b], ((n >> 1) - 1) & 1, abort_flag))) break;
+        if (n >= 2 && !(ok = wait_lanes(&ml_empty[b], ((n >> 1) - 1) & 1, abort_flag))) break;
         ml[b * 128 + r] = make_float4(m, l + ps, ps, 0.f);
         mbar_arrive(&ml_full[b]);
       }
@@ -466,14 +467,14 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     const uint32_t tO = tbase + lane_off + kPwColO;
     int n = 0;
     bool ok = true;
-    for (int item = 0; ok && pg_item(queue, i_full, item, abort_flag); ++item) {
+    for (int item = 0; ok && pg_item<true>(queue, i_full, item, abort_flag); ++item) {
       const PgItem& it = queue.it[item % kPgItems];
       const int nblk = blocks_of(it);
       for (int blk = 0; ok && blk < nblk; ++blk, ++n) {
         const int b = n & 1;
-        if (!(ok = wait_bounded(o_full, n & 1, abort_flag))) break;
+        if (!(ok = wait_lanes(o_full, n & 1, abort_flag))) break;
         tc_fence_after();
-        if (!(ok = wait_bounded(&ml_full[b], (n >> 1) & 1, abort_flag))) break;
+        if (!(ok = wait_lanes(&ml_full[b], (n >> 1) & 1, abort_flag))) break;
         const float4 mlv = ml[b * 128 + r];  // m (base 2), unrounded sum with the sink, the sink's term
         mbar_arrive(&ml_empty[b]);
         float rs[16];
@@ -496,39 +497,41 @@ __global__ void __launch_bounds__(kPwThreads, 1)
             tc_fence_before();
             mbar_arrive(o_empty);
           }
-          if (!live) continue;
+          if (live) {
 #pragma unroll
-          for (int e = 0; e < 64; ++e) odd = fmaf(o[e], 0.f, odd);
-          if (p.out_f32) {
-            float* dst = reinterpret_cast<float*>(p.out) + ob + h * 64;
+            for (int e = 0; e < 64; ++e) odd = fmaf(o[e], 0.f, odd);
+            if (p.out_f32) {
+              float* dst = reinterpret_cast<float*>(p.out) + ob + h * 64;
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              reinterpret_cast<float4*>(dst)[e] =
-                  make_float4(o[4 * e] * f, o[4 * e + 1] * f, o[4 * e + 2] * f, o[4 * e + 3] * f);
-          } else if (p.out_v8) {
-            __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.out) + ob + h * 64;
+              for (int e = 0; e < 16; ++e)
+                reinterpret_cast<float4*>(dst)[e] =
+                    make_float4(o[4 * e] * f, o[4 * e + 1] * f, o[4 * e + 2] * f, o[4 * e + 3] * f);
+            } else if (p.out_v8) {
+              __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.out) + ob + h * 64;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              st_global_v8(dst + 16 * e, pack_bf16(o[16 * e + 0] * f, o[16 * e + 1] * f),
-                           pack_bf16(o[16 * e + 2] * f, o[16 * e + 3] * f),
-                           pack_bf16(o[16 * e + 4] * f, o[16 * e + 5] * f),
-                           pack_bf16(o[16 * e + 6] * f, o[16 * e + 7] * f),
-                           pack_bf16(o[16 * e + 8] * f, o[16 * e + 9] * f),
-                           pack_bf16(o[16 * e + 10] * f, o[16 * e + 11] * f),
-                           pack_bf16(o[16 * e + 12] * f, o[16 * e + 13] * f),
-                           pack_bf16(o[16 * e + 14] * f, o[16 * e + 15] * f));
-          } else {
-            uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.out) + ob + h * 64);
+              for (int e = 0; e < 4; ++e)
+                st_global_v8(dst + 16 * e, pack_bf16(o[16 * e + 0] * f, o[16 * e + 1] * f),
+                             pack_bf16(o[16 * e + 2] * f, o[16 * e + 3] * f),
+                             pack_bf16(o[16 * e + 4] * f, o[16 * e + 5] * f),
+                             pack_bf16(o[16 * e + 6] * f, o[16 * e + 7] * f),
+                             pack_bf16(o[16 * e + 8] * f, o[16 * e + 9] * f),
+                             pack_bf16(o[16 * e + 10] * f, o[16 * e + 11] * f),
+                             pack_bf16(o[16 * e + 12] * f, o[16 * e + 13] * f),
+                             pack_bf16(o[16 * e + 14] * f, o[16 * e + 15] * f));
+            } else {
+              uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.out) + ob + h * 64);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              uint4 u;
-              u.x = pack_bf16(o[8 * e + 0] * f, o[8 * e + 1] * f);
-              u.y = pack_bf16(o[8 * e + 2] * f, o[8 * e + 3] * f);
-              u.z = pack_bf16(o[8 * e + 4] * f, o[8 * e + 5] * f);
-              u.w = pack_bf16(o[8 * e + 6] * f, o[8 * e + 7] * f);
-              dst[e] = u;
+              for (int e = 0; e < 8; ++e) {
+                uint4 u;
+                u.x = pack_bf16(o[8 * e + 0] * f, o[8 * e + 1] * f);
+                u.y = pack_bf16(o[8 * e + 2] * f, o[8 * e + 3] * f);
+                u.z = pack_bf16(o[8 * e + 4] * f, o[8 * e + 5] * f);
+                u.w = pack_bf16(o[8 * e + 6] * f, o[8 * e + 7] * f);
+                dst[e] = u;
+              }
             }
           }
+          __syncwarp();  // TMEM is read by the whole warp
         }
         // 0 * v is NaN where v is not finite, so such a value of a key that the row
         // does not see, and another row of the item does, is in its sum
@@ -536,6 +539,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         if (live && p.lse)
           p.lse[(size_t)hg * p.pb.total_q + tok] =
               (mlv.y != 0.f) ? (mlv.x * 0.6931471805599453f + logf(mlv.y)) : -INFINITY;
+        __syncwarp();  // the rows done again take their own time
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&i_empty[item % kPgItems]);

@@ -1,0 +1,34 @@
+"""Edges of the paged cache on the GPU: rows of one warp that part ways.  Inputs and
+tolerances as in tests/test_paged_gpu.py."""
+
+import numpy as np
+import pytest
+import torch
+
+from tests import parity_util as P
+from tests.test_paged_gpu import attend, build, oracle_of
+
+pytestmark = pytest.mark.gpu
+
+
+# windows whose items are one block and two; rows of a warp that hold no token, beside
+# rows that are done again (a value that is not finite, hidden from some of them)
+@pytest.mark.parametrize("lens,news,window,hq,hkv", [
+    ([300, 90, 40], [13, 29, 5], 129, 16, 1), ([300, 90], [37, 45], 120, 48, 4), ([200, 60], [33, 11], 100, 7, 1),
+    ([260, 31], [90, 31], 9, 3, 3)])
+@pytest.mark.parametrize("odt", [torch.float32, torch.bfloat16])
+def test_rows_of_a_warp_that_part_ways(lens, news, window, hq, hkv, odt):
+    x = build(lens, news, window, 16, hq, hkv, seed=sum(news))
+    for b, (L, n) in enumerate(zip(lens, news)):
+        for p in (L - n, L - n // 2, L - 1):
+            x["vp"][int(x["table"][b, p // 16]), p % 16, :, ::40] = float("nan")
+    want, want_lse, mass = oracle_of(x)
+    out, lse = attend(x, out_dtype=odt)
+    o = P.to64(out)
+    fine = np.isfinite(want)
+    assert np.array_equal(np.isfinite(o), fine)
+    bound = 2.0 ** -8 * (mass + np.abs(want)) + 5.2e-4 * mass + 1e-6
+    if odt == torch.bfloat16:
+        bound = bound + 2.0 ** -8 * (np.abs(want) + bound)
+    assert np.all(np.abs(o - want)[fine] <= bound[fine])
+    assert np.max(np.abs(P.to64(lse) - want_lse)) <= 3e-4

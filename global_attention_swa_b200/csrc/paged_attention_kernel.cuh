@@ -177,7 +177,7 @@ struct PgItem {
   int tok0;         // packed row of its first token
   int p0;           // that token's position
   int tokens;       // valid tokens, 1 .. kTiles * TQ
-  int outer;        // the first or last item of the sequence's chunk
+  int outer;        // of its boxes of 16 keys, some reach past the sequence's end or before its chunk's first key
   int lo, hi;       // keys that some row sees: [lo, hi]
   int early;        // of those, [lo, early) and (p0, hi] are hidden from some rows
   int start;        // first key of tile 0: lo rounded down to a box
@@ -242,11 +242,11 @@ struct PgWalk {
       it.tok0 = s.b0 + at.i * D;
       it.p0 = s.len - s.n + at.i * D;
       it.tokens = min(D, s.n - at.i * D);
-      it.outer = at.i == 0 || it.hi + 1 == s.len;
       it.hi = it.p0 + it.tokens - 1;
       it.lo = p.window > 0 ? max(0, it.p0 - p.window + 1) : 0;
       it.early = p.window > 0 ? max(it.lo, it.hi - p.window + 1) : it.lo;
       it.start = it.lo / p.box_rows * p.box_rows;
+      it.outer = it.start < max(0, s.len - s.n - p.window + 1) || it.start + ((it.hi - it.start + 16) & ~15) > s.len;
       it.n_kt = (it.hi - it.start) / kPgKeys + 1;
       const int left = it.hi + 1 - (it.start + (it.n_kt - 1) * kPgKeys);
       it.n_last = min(kPgKeys, (left + 15) & ~15);

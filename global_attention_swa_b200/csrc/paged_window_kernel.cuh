@@ -64,14 +64,12 @@ static_assert(kPwOffOnes % 1024 == 0 && kPwColSum + 16 <= 512 && kPwSmemBytes <=
 __device__ __forceinline__ PgTile pw_keys(const PgItem& it) { return pg_keys(it, it.start, kPwKeys); }
 
 // Rows past the sequence's end, and before the first key that its chunk sees, may
-// never have been written: they are zeroed before the product.  Other rows that
-// nothing of the item sees are, nearly all, seen by another item, and stay: what is
-// not finite among them is met as in any hidden key (pw_row_again), and V goes to its
-// products without a warp between (with an item fetched ahead by the issuer, 69.5
+// never have been written: they are zeroed before the product, with all that nothing
+// of such an item sees.  Elsewhere such rows are seen by another item, and stay: what
+// is not finite among them is met as in any hidden key (pw_row_again), and V goes to
+// its products without a warp between (with an item fetched ahead by the issuer, 69.5
 // against 72.5 us).
-__device__ __forceinline__ bool pw_open(const PgItem& it, const PgTile& keys) {
-  return it.outer && (keys.zlo > 0 || keys.zhi < keys.n);
-}
+__device__ __forceinline__ bool pw_open(const PgItem& it) { return it.outer; }
 
 // One row (packed row tok, head h, position pos) from the definition, its output
 // only: keys that it does not see take no part at all.  For rows whose product
@@ -300,7 +298,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         const int nblk = blocks_of(it);
         const PgTile keys = pw_keys(it);
         const int k = keys.n;
-        const bool open = pw_open(it, keys);
+        const bool open = pw_open(it);
         const uint32_t idesc_s = idesc_bf16_f32(128, 0, false, false) | (static_cast<uint32_t>(k >> 3) << 17);
         for (int blk = 0; ok && blk < nblk; ++blk, ++n) {
           const int b = n & 1;
@@ -349,7 +347,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         for (int c = 0; c < 2; ++c)
           tma_load_3d(smem + kPwOffV + c * kPwKBox + lane * kPwBoxRows * 128, &tm_v, v_full, c * 64, it.g, row);
       }
-      if (pw_open(it, keys)) {
+      if (pw_open(it)) {
         if (!wait_warp(v_full, kp & 1, abort_flag)) break;
         pg_zero_unseen(keys, sbase + kPwOffV, kPwKBox);
         fence_proxy_async_smem();

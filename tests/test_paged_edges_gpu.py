@@ -1,4 +1,5 @@
-"""Edges of the paged cache on the GPU: rows of one warp that part ways.  Inputs and
+"""Edges of the paged cache on the GPU: rows of one warp that part ways, slots that
+nothing sees.  Inputs and
 tolerances as in tests/test_paged_gpu.py."""
 
 import numpy as np
@@ -6,7 +7,7 @@ import pytest
 import torch
 
 from tests import parity_util as P
-from tests.test_paged_gpu import attend, build, oracle_of
+from tests.test_paged_gpu import attend, build, check, oracle_of
 
 pytestmark = pytest.mark.gpu
 
@@ -32,3 +33,19 @@ def test_rows_of_a_warp_that_part_ways(lens, news, window, hq, hkv, odt):
         bound = bound + 2.0 ** -8 * (np.abs(want) + bound)
     assert np.all(np.abs(o - want)[fine] <= bound[fine])
     assert np.max(np.abs(P.to64(lse) - want_lse)) <= 3e-4
+
+
+@pytest.mark.parametrize("lens,news,window,hq,hkv", [
+    ([701, 333], [77, 161], 129, 16, 1), ([95], [90], 129, 32, 2), ([333, 61], [100, 60], 40, 7, 1), ([500], [300], 9, 2, 2),
+    ([333, 90], [30, 11], 100, 64, 1), ([333, 90], [30, 11], 33, 128, 1)])  # items of fewer tokens than a box
+@pytest.mark.parametrize("odt", [torch.float32, torch.bfloat16])
+def test_slots_that_nothing_sees_do_not_show(lens, news, window, hq, hkv, odt):
+    """Chunks of several items: the slots before the first key and past the end change no
+    bit of the result, written or not."""
+    x = build(lens, news, window, 16, hq, hkv, seed=len(lens))
+    assert torch.isnan(x["vp"][int(x["table"][0, (lens[0] - 1) // 16]), lens[0] % 16:]).all() and lens[0] % 16
+    out, lse = attend(x, out_dtype=odt)
+    x["kp"], x["vp"] = x["kp"].nan_to_num(0.0), x["vp"].nan_to_num(0.0)
+    want, want_lse = attend(x, out_dtype=odt)
+    check(want, want_lse, oracle_of(x))
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)

@@ -1019,14 +1019,14 @@ mimo_status_t ensure_paged_attributes() {
 }
 
 // The arrays of the page bookkeeping calls.  Their kernels count in int32 a
-// stride past the last element.
+// stride past the last element (but for pairs, which they count in 64 bits).
 constexpr long kMaxTableEntries = 1L << 30;
 mimo_status_t check_page_table(const int32_t* page_refs, int num_pages, const int32_t* block_table,
                                int num_seqs, int max_pages, const int32_t* refs_out, const int32_t* table_out) {
   if (num_pages <= 0) return fail(MIMO_ERR_INVALID_ARG, "num_pages must be positive (got %d)", num_pages);
   if (num_seqs < 0 || max_pages < 0) return fail(MIMO_ERR_INVALID_ARG, "sizes must be non-negative");
-  if ((long)num_seqs * max_pages > kMaxTableEntries || num_pages > kMaxTableEntries)
-    return fail(MIMO_ERR_UNSUPPORTED, "num_seqs * max_pages and num_pages must be at most 2^30");
+  if ((long)num_seqs * std::max(max_pages, 1) > kMaxTableEntries || num_pages > kMaxTableEntries)
+    return fail(MIMO_ERR_UNSUPPORTED, "num_seqs, num_seqs * max_pages and num_pages must be at most 2^30");
   const bool entries = num_seqs > 0 && max_pages > 0;
   if (!page_refs || !refs_out || (entries && (!block_table || !table_out)))
     return fail(MIMO_ERR_INVALID_ARG, "page_refs, block_table and their outputs must be non-NULL");
@@ -1296,8 +1296,8 @@ mimo_status_t mimo_attn_page_fork(const int32_t* page_refs, int num_pages, const
   const int32_t* out = num_seqs_out > 0 ? block_table_out : block_table;
   mimo_status_t st = check_page_table(page_refs, num_pages, block_table, num_seqs, max_pages, page_refs_out, out);
   if (st) return st;
-  if ((long)num_seqs_out * max_pages > kMaxTableEntries)
-    return fail(MIMO_ERR_UNSUPPORTED, "num_seqs_out * max_pages must be at most 2^30");
+  if ((long)num_seqs_out * std::max(max_pages, 1) > kMaxTableEntries)
+    return fail(MIMO_ERR_UNSUPPORTED, "num_seqs_out and num_seqs_out * max_pages must be at most 2^30");
   if (num_seqs_out > 0 && max_pages > 0 && (!parent || !block_table_out || !aligned4(parent) || !aligned4(block_table_out)))
     return fail(MIMO_ERR_INVALID_ARG, "parent and block_table_out must be non-NULL and 4-byte aligned");
   if (num_seqs > 0 && num_seqs_out > 0 && max_pages > 0 &&

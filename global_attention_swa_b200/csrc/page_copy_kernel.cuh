@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(kPcThreads) page_copy_kernel(const PageCopyPar
     const int piece = (int)(u % p.pieces);
     const long long r = u / p.pieces;
     const int layer = (int)(r % p.layers), m = (int)(r / p.layers);
-    const int src = p.moves[2 * m], dst = p.moves[2 * m + 1];
+    const int src = p.moves[2LL * m], dst = p.moves[2LL * m + 1];
     if (src < 0 || dst < 0 || src >= p.P || dst >= p.P) {
       if ((src >= p.P || dst >= p.P || (src < 0) != (dst < 0)) && threadIdx.x == 0)
         record_status(1 /* MIMO_ERR_INVALID_ARG */);

@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) page_hold_kernel(const PageHold
 
   if (p.refs_out != p.refs)
     for (int i = tid; i < p.P; i += threads) p.refs_out[i] = p.refs[i];
-  for (int i = tid; i < 2 * p.B; i += threads) p.moves[i] = -1;
+  for (long long i = tid; i < 2LL * p.B; i += threads) p.moves[i] = -1;
   if (tid == 0) p.ws[0] = 0;
   cluster_sync_all();
 
@@ -298,8 +298,8 @@ __global__ void __launch_bounds__(kPtThreads, 1) page_hold_kernel(const PageHold
           if (v <= -2) {
             if (atomicSub(&p.refs_out[-2 - v], 1) == 1) atomicAdd(&p.ws[0], 1);
             if ((long long)c.j * p.page_size < c.row.write_from) {  // at most one page of a sequence
-              p.moves[2 * c.b] = -2 - v;
-              p.moves[2 * c.b + 1] = pg;
+              p.moves[2LL * c.b] = -2 - v;
+              p.moves[2LL * c.b + 1] = pg;
             }
           }
         } else if (in && v >= 0 && !c.wanted()) {
@@ -347,8 +347,8 @@ __global__ void __launch_bounds__(kPtThreads, 1) page_fork_kernel(const PageFork
     for (int i = threadIdx.x; i < rows; i += kPtThreads) children[i] = 0;
     __syncthreads();
     for (int i = threadIdx.x; i < p.B_out; i += kPtThreads) {
-      const int r = p.parent[i] - r0;
-      if (r >= 0 && r < rows) atomicAdd(&children[r], 1);
+      const int r = p.parent[i];
+      if (r >= r0 && r < r0 + rows) atomicAdd(&children[r - r0], 1);
     }
     __syncthreads();
     const int step_b = kPtThreads / max(1, p.M), step_j = kPtThreads - step_b * p.M;
@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) page_compact_kernel(const PageC
     ks += __popc(s);
     kd += __popc(d);
   }
-  for (int i = 2 * count + tid; i < 2 * p.max_moves; i += threads) p.moves[i] = -1;
+  for (long long i = 2LL * count + tid; i < 2LL * p.max_moves; i += threads) p.moves[i] = -1;
   cluster_sync_all();
 
   for (int k = tid; k < count; k += threads) {

@@ -407,8 +407,8 @@ mimo_status_t mimo_attn_paged_append(const mimo_attn_dims_t* dims, const void* q
 
 /*
  * Page bookkeeping, wholly on the device (nothing is read back, so the calls can
- * be captured in a graph); num_pages and num_seqs * max_pages are at most 2^30
- * (else MIMO_ERR_UNSUPPORTED).  page_refs_out may be page_refs and, but for fork,
+ * be captured in a graph); num_pages, num_seqs (num_seqs_out) and num_seqs *
+ * max_pages are at most 2^30 (else MIMO_ERR_UNSUPPORTED).  page_refs_out may be page_refs and, but for fork,
  * block_table_out may be block_table (in place); otherwise the outputs must
  * not overlap the inputs.  Results are deterministic.  block_table entries at
  * or above num_pages are recorded as MIMO_ERR_INVALID_ARG and count as no page

@@ -400,7 +400,8 @@ __global__ void __launch_bounds__(kPwThreads, 1)
           // visible columns' maximum, and stands while no column exceeds it by more than
           // 64: P is as exact against any reference that neither overflows nor vanishes.
           // Else it moves up by a whole number, by which the P stored so far are scaled
-          // exactly.
+          // exactly; or by more than 256 to the maximum itself, where nothing is left of
+          // them (and the rounding of a sum with a far m would be the scores' loss).
           float2 l2 = make_float2(0.f, 0.f);
           const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
 #pragma unroll 1
@@ -420,7 +421,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
             const float mx = fmaxf(mx0, mx1) * p.scale_log2;
             const bool low = mx > m + 64.f;
             if (__any_sync(0xffffffffu, low)) {
-              const float up = m == -INFINITY ? mx : m + ceilf(mx - m);
+              const float up = mx - m > 256.f ? mx : m + ceilf(mx - m);  // infinity too
               const float f = !low || m == -INFINITY ? 1.f : ex2(m - up);  // without a reference all P are 0
               if (low) m = up;
               if (c0 > 0 && __any_sync(0xffffffffu, f != 1.f)) {

@@ -1,6 +1,6 @@
 """Edges of the paged cache on the GPU: rows of one warp that part ways, slots that
-nothing sees.  Inputs and
-tolerances as in tests/test_paged_gpu.py."""
+nothing sees, sinks far below the scores.  Inputs and tolerances as in
+tests/test_paged_gpu.py."""
 
 import numpy as np
 import pytest
@@ -49,3 +49,20 @@ def test_slots_that_nothing_sees_do_not_show(lens, news, window, hq, hkv, odt):
     want, want_lse = attend(x, out_dtype=odt)
     check(want, want_lse, oracle_of(x))
     assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("sink", [-1e10, -1e30, float(np.finfo(np.float32).min)])
+@pytest.mark.parametrize("window", [0, 129])
+@pytest.mark.parametrize("lens,n,times", [([700, 30], 1, 64), ([700, 30], 6, 64), ([300, 30], 30, 64), ([9, 5], 5, 256)])
+def test_a_sink_out_of_sight_beside_large_scores(lens, n, times, window, sink):
+    """A sink so low that the gap to the scores does not keep their digits: scores of
+    hundreds, of either sign, decide alone."""
+    x = build(lens, [n] * len(lens), window, 16, 16, 1, seed=12)
+    x["q"] *= times
+    x["sinks"] = torch.full((16,), sink)
+    out, lse = attend(x, out_dtype=torch.float32)
+    want, want_lse, mass = oracle_of(x)
+    assert want_lse.max() > 100 and (times == 64 or want_lse.min() < -100)
+    # the scores are `times` those of the module's bound, so is their error
+    assert np.all(np.abs(P.to64(out) - want) <= 2.0 ** -8 * (mass + np.abs(want)) + times * 5.2e-4 * mass + 1e-6)
+    assert np.max(np.abs(P.to64(lse) - want_lse)) <= times * 3e-4

@@ -118,10 +118,12 @@ struct PgPlace {
 // Cost of an item of a sequence, in keys: what it reads, and kPgItemCost for
 // its queries, its latencies and its epilogue (a fit over the CTAs of a batch of
 // drafts: 1.6 us a key tile, 4.7 an item).
-// In a window that is the same for all blocks; without one, block i reads
-// first + D (i + 1) keys (first: the position of the chunk's first token, D:
-// tokens of a block).  With whole items only, 1.  (Those drafts take 133 us with
-// a cost of three key tiles, 134 with two, 135 with four, 142 without.)
+// Block i reads the D (i + 1) keys of the chunk up to its own (D: tokens of a block)
+// and those before the chunk, but no more of the keys before it than its window: the
+// cost rises by D a block as long as the window reaches back to the sequence's first
+// key, and is the same for all blocks from there on.  With whole items only, 1.
+// (Those drafts take 133 us with a cost of three key tiles, 134 with two, 135 with
+// four, 142 without.)
 constexpr int kPgItemCost = 3 * kPgKeys;
 // Quotient of non-negative values; nearly always both fit 32 bits, and a 64-bit
 // division is a long chain of dependent instructions.
@@ -132,24 +134,25 @@ __device__ __forceinline__ long long pg_div(long long a, long long b) {
 
 struct PgCost {
   long long base;  // block 0
-  int slope;       // each further block
+  int slope;       // each further one of the first `rising`
+  int rising;
   int blocks;
+  long long flat;  // each block from there on
   __device__ __forceinline__ long long upto(int i) const {  // blocks 0 .. i-1
-    return base * i + (long long)slope * ((long long)i * (i - 1) / 2);
+    const int r = min(i, rising);
+    return base * r + (long long)slope * ((long long)r * (r - 1) / 2) + flat * (i - r);
   }
   // the block that holds cost y of [0, upto(blocks))
   __device__ __forceinline__ int block_of(long long y) const {
     if (blocks <= 1) return 0;
-    int i;
-    if (slope == 0) {
-      i = (int)pg_div(y, base);
-    } else {  // the root of upto(i) = y, near enough for the steps below to find it
-      const float h = (float)base - 0.5f * slope, z = 2.f * (float)y;
-      i = (int)(z / (sqrtf(h * h + slope * z) + h));
-    }
-    i = max(0, min(i, blocks - 1));
+    const long long rise = upto(rising);
+    if (y >= rise) return min(blocks - 1, rising + (int)pg_div(y - rise, flat));
+    // the root of upto(i) = y, near enough for the steps below to find it
+    const float h = (float)base - 0.5f * slope, z = 2.f * (float)y;
+    int i = (int)(z / (sqrtf(h * h + slope * z) + h));
+    i = max(0, min(i, rising - 1));
     while (i > 0 && upto(i) > y) --i;
-    while (i + 1 < blocks && upto(i + 1) <= y) ++i;
+    while (i + 1 < rising && upto(i + 1) <= y) ++i;
     return i;
   }
 };
@@ -158,15 +161,16 @@ __device__ __forceinline__ PgCost pg_cost(const PagedAttnParams& p, const PagedS
   PgCost c;
   const int D = kTiles * p.TQ;
   c.blocks = s.ok ? (s.n + D - 1) / D : 0;
+  c.slope = D;
+  c.base = (long long)(s.len - s.n) + D + kPgItemCost;
+  c.rising = c.blocks;
+  c.flat = 1;
   if (!p.split) {
-    c.base = 1;
-    c.slope = 0;
-  } else if (p.window > 0) {
-    c.base = (long long)p.window + D + kPgItemCost;
-    c.slope = 0;
-  } else {
-    c.base = (long long)(s.len - s.n) + D + kPgItemCost;
-    c.slope = D;
+    c.rising = 0;
+  } else if (p.window > 0) {  // block i begins at position first + D i
+    const int first = s.len - s.n;
+    c.rising = first >= p.window ? 0 : min(c.blocks, (p.window - first - 1) / D + 1);
+    c.flat = (long long)p.window + D + kPgItemCost;
   }
   return c;
 }

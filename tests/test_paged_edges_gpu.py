@@ -1,6 +1,6 @@
 """Edges of the paged cache on the GPU: rows of one warp that part ways, slots that
-nothing sees, sinks far below the scores.  Inputs and tolerances as in
-tests/test_paged_gpu.py."""
+nothing sees, sinks far below the scores, windows longer than a sequence.  Inputs and
+tolerances as in tests/test_paged_gpu.py."""
 
 import numpy as np
 import pytest
@@ -66,3 +66,23 @@ def test_a_sink_out_of_sight_beside_large_scores(lens, n, times, window, sink):
     # the scores are `times` those of the module's bound, so is their error
     assert np.all(np.abs(P.to64(out) - want) <= 2.0 ** -8 * (mass + np.abs(want)) + times * 5.2e-4 * mass + 1e-6)
     assert np.max(np.abs(P.to64(lse) - want_lse)) <= times * 3e-4
+
+
+@pytest.mark.parametrize("lens,news", [([5000, 300], [1, 1]), ([5000, 900, 40], [6, 3, 6]), ([2600], [300]),
+                                       ([2000, 2000, 70], [40, 2000, 70])])
+def test_a_window_past_the_length_is_no_window(lens, news):
+    """Nothing is hidden, so the work is dealt out as without one: the same bits."""
+    x = build(lens, news, 0, 64, 16, 1, seed=sum(lens))
+    want, want_lse = attend(x, out_dtype=torch.float32)
+    for window in (max(lens), 6000, 2 ** 31 - 1):
+        x["window"] = window
+        out, lse = attend(x, out_dtype=torch.float32)
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("lens,news,window,hq", [([1500], [900], 700, 16), ([1500, 40, 900], [1100, 3, 1], 600, 16),
+                                                 ([2500, 300], [300, 300], 1000, 6), ([700, 900], [700, 17], 650, 64)])
+def test_chunks_that_grow_into_their_window(lens, news, window, hq):
+    """First blocks that see less than a window, and later ones that see a whole one."""
+    x = build(lens, news, window, 16, hq, 1, seed=window)
+    check(*attend(x), oracle_of(x))

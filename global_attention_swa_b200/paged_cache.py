@@ -78,7 +78,8 @@ class PagedCache:
         extended, and records that too.  Returns ``info``."""
         lens = self.seqlens + new_tokens
         first = self._first()
-        moves = self._hold(lens, first, self.seqlens)
+        # a sequence without new tokens writes nothing and parts from no page
+        moves = self._hold(lens, first, torch.where(new_tokens > 0, self.seqlens, self.capacity))
         mimo.mimo_attn_page_copy(self.k_pages, self.v_pages, moves)
         done = (self.info[0] == 0) & (lens >= 0) & (lens <= self.capacity)
         self._attend.copy_(torch.where(done, lens, -1))

@@ -1,15 +1,19 @@
 """Edges of the paged cache on the GPU: rows of one warp that part ways, slots that
-nothing sees, sinks far below the scores, windows longer than a sequence.  Inputs and
-tolerances as in tests/test_paged_gpu.py."""
+nothing sees, sinks far below the scores, windows longer than a sequence, and turns in
+the life of a PagedCache.  Inputs and tolerances as in tests/test_paged_gpu.py."""
 
 import numpy as np
 import pytest
 import torch
 
 from tests import parity_util as P
-from tests.test_paged_gpu import attend, build, check, oracle_of
+from tests.test_paged_gpu import attend, build, check, ints, oracle_of
 
 pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import global_attention_swa_b200 as mimo
+    from global_attention_swa_b200.paged_cache import PagedCache
 
 
 # windows whose items are one block and two; rows of a warp that hold no token, beside
@@ -86,3 +90,18 @@ def test_chunks_that_grow_into_their_window(lens, news, window, hq):
     """First blocks that see less than a window, and later ones that see a whole one."""
     x = build(lens, news, window, 16, hq, 1, seed=window)
     check(*attend(x), oracle_of(x))
+
+
+def test_a_fork_that_stands_still_needs_no_page():
+    """Only the slots that get tokens part from the shared page: four beams, one free page,
+    one beam goes on."""
+    cache = PagedCache(1, 3, 16, 4, 3, 1)
+    cache.extend(ints([20, 0, 0, 0]).cuda())
+    cache.fork(ints([0, 0, 0, 0]).cuda())
+    shared = cache.block_table[0, :2].tolist()
+    info = cache.extend(ints([0, 1, 0, 0]).cuda())
+    mimo.mimo_attn_device_status()
+    assert info.tolist() == [0, 0] and cache.seqlens.tolist() == [20, 21, 20, 20]
+    table = cache.block_table[:, :2].tolist()
+    assert [table[i] for i in (0, 2, 3)] == [shared] * 3 and table[1] == [shared[0], ({0, 1, 2} - set(shared)).pop()]
+    assert cache.page_refs[shared].tolist() == [4, 3]

@@ -50,7 +50,7 @@ class PagedCache:
         self._spare_table = torch.empty_like(self.block_table)
         self.seqlens = torch.zeros(num_seqs, **ints)
         self.info = torch.zeros(2, **ints)
-        self._attend = torch.zeros(num_seqs, **ints)  # what attend goes by: -1 where extend found no room
+        self._attend = torch.zeros(num_seqs, **ints)  # what attend goes by: -1 since extend found no room
         self._kept = torch.zeros(num_seqs, **ints)  # first position whose page was never released
         self.page_size, self.window, self.rollback = page_size, window, rollback
         self.capacity = max_pages * page_size
@@ -75,7 +75,7 @@ class PagedCache:
         nothing changes and ``info[0]`` says how many were missing; a sequence that
         would pass max_pages pages stays as it is and is recorded as an invalid
         argument in the device status.  ``attend`` skips sequences that were not
-        extended, and records that too.  Returns ``info``."""
+        extended, until they are, and records that too.  Returns ``info``."""
         lens = self.seqlens + new_tokens
         first = self._first()
         # a sequence without new tokens writes nothing and parts from no page
@@ -110,7 +110,7 @@ class PagedCache:
         # what extend kept stays, so that a later call may go back further
         self._hold(lens, self._kept if self.window else None, None)
         self.seqlens.copy_(torch.where(lens >= 0, lens, self.seqlens))  # a negative one was recorded
-        self._attend.copy_(self.seqlens)
+        self._attend.copy_(torch.where(self._attend < 0, self._attend, self.seqlens))
         self._kept.mul_(lens != 0)
         return self.info
 
@@ -123,9 +123,8 @@ class PagedCache:
         self.block_table.copy_(self._spare_table)
         slots = self.seqlens.numel()
         source, real = parent.clamp(0, slots - 1).long(), (parent >= 0) & (parent < slots)
-        for t in (self.seqlens, self._kept):
+        for t in (self.seqlens, self._kept, self._attend):
             t.copy_(t[source] * real)
-        self._attend.copy_(self.seqlens)
 
     def compact(self, max_moves):
         """Move used pages from the end of the pools to free places at their front, at most

@@ -105,3 +105,49 @@ def test_a_fork_that_stands_still_needs_no_page():
     table = cache.block_table[:, :2].tolist()
     assert [table[i] for i in (0, 2, 3)] == [shared] * 3 and table[1] == [shared[0], ({0, 1, 2} - set(shared)).pop()]
     assert cache.page_refs[shared].tolist() == [4, 3]
+
+
+@pytest.mark.parametrize("change", ["truncate", "fork"])
+def test_a_sequence_without_room_stays_skipped_until_it_is_extended(change):
+    """The pool has no page for slot 1's next tokens; freeing slot 0 does not give them to
+    it: attend leaves what is there as it is until extend has."""
+    g = torch.Generator().manual_seed(5)
+
+    def chunk(n):
+        return [torch.randn((n, h, d), generator=g).to(torch.bfloat16).cuda() for h, d in ((8, 192), (2, 192), (2, 128))]
+
+    cache = PagedCache(1, 5, 16, 2, 5, 2)
+    cache.extend(ints([40, 30]).cuda())
+    cache.attend(0, *chunk(70), ints([0, 40, 70]).cuda(), 40, None, 1e4)
+    assert cache.extend(ints([0, 8]).cuda())[0] == 1
+    if change == "truncate":
+        cache.truncate(ints([0, 30]).cuda())
+    else:
+        cache.fork(ints([-1, 1]).cuda())
+    mimo.mimo_attn_device_status()
+    k, v = cache.k_pages.clone(), cache.v_pages.clone()
+    rows = chunk(8)
+    cache.attend(0, *rows, ints([0, 0, 8]).cuda(), 8, None, 1e4)
+    with pytest.raises(mimo.MimoAttnError) as e:
+        mimo.mimo_attn_device_status()
+    assert e.value.status == mimo.MIMO_ERR_INVALID_ARG
+    assert torch.equal(cache.k_pages, k) and torch.equal(cache.v_pages, v)
+    assert cache.extend(ints([0, 8]).cuda())[0] == 0 and cache.seqlens.tolist() == [0, 38]
+    out, _ = cache.attend(0, *rows, ints([0, 0, 8]).cuda(), 8, None, 1e4)
+    mimo.mimo_attn_device_status()
+    assert torch.isfinite(out).all() and torch.equal(cache.v_pages[0, cache.block_table[1, 2].long(), :6], rows[2][2:])
+    assert torch.equal(cache.v_pages[0, cache.block_table[1, 1].long(), :14], v[0, cache.block_table[1, 1].long(), :14])
+
+
+def test_room_that_is_given_back_before_it_is_used():
+    """extend for the most drafted tokens, truncate to those there are, then attend."""
+    g = torch.Generator().manual_seed(6)
+    cache = PagedCache(1, 8, 16, 2, 4, 1)
+    cache.extend(ints([9, 9]).cuda())
+    cache.truncate(ints([5, 3]).cuda())
+    q, k, v = (torch.randn((8, h, d), generator=g).to(torch.bfloat16).cuda() for h, d in ((4, 192), (1, 192), (1, 128)))
+    cache.attend(0, q, k, v, ints([0, 5, 8]).cuda(), 5, None)
+    mimo.mimo_attn_device_status()
+    for b, rows in enumerate((slice(0, 5), slice(5, 8))):
+        page = int(cache.block_table[b, 0])
+        assert torch.equal(cache.v_pages[0, page, :rows.stop - rows.start], v[rows])

@@ -89,18 +89,21 @@ class PagedCache:
         return self.info
 
     def attend(self, layer, q, k, v, cu_seqlens_q, max_seqlen_q, sinks, rope_theta=None, rotary_dim=None,
-               out_dtype=torch.bfloat16, softmax_scale=None, v_scale=1.0):
+               out_dtype=torch.bfloat16, softmax_scale=None, v_scale=1.0, out=None, lse=None):
         """One layer's attention of the tokens that ``extend`` made room for: q and k are
         rotated (rope_theta None: they already are), k and v written, and q attends over
-        the cache.  Rows are packed by cu_seqlens_q.  Returns (out [Nt,Hq,128], lse [Hq,Nt])."""
+        the cache.  Rows are packed by cu_seqlens_q.  Returns (out [Nt,Hq,128], lse [Hq,Nt]):
+        the tensors given, or new ones.  Rows of skipped sequences, and of none, are left
+        as they were: in new tensors they hold no particular values, so a step that goes on
+        past a failed ``extend`` brings tensors of its own."""
         kp, vp = self.k_pages[layer], self.v_pages[layer]
         q = mimo.mimo_attn_paged_append(q, k, v, kp, vp, self.block_table, cu_seqlens_q, self._attend,
                                         1.0 if rope_theta is None else rope_theta,
                                         0 if rope_theta is None else rotary_dim,
                                         q_out=q if rope_theta is None else None)
         return mimo.mimo_attn_paged_attention(q, kp, vp, self.block_table, cu_seqlens_q, self._attend,
-                                              max_seqlen_q, self.window, sinks, out_dtype=out_dtype,
-                                              softmax_scale=softmax_scale, v_scale=v_scale)
+                                              max_seqlen_q, self.window, sinks, out=out, lse=lse,
+                                              out_dtype=out_dtype, softmax_scale=softmax_scale, v_scale=v_scale)
 
     def truncate(self, lens):
         """Take the sequences back to lens [num_seqs] int32 (at most their present length):

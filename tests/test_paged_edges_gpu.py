@@ -151,3 +151,25 @@ def test_room_that_is_given_back_before_it_is_used():
     for b, rows in enumerate((slice(0, 5), slice(5, 8))):
         page = int(cache.block_table[b, 0])
         assert torch.equal(cache.v_pages[0, page, :rows.stop - rows.start], v[rows])
+
+
+@pytest.mark.parametrize("window", [0, 129])
+def test_rows_of_skipped_sequences_stay_as_the_caller_had_them(window):
+    """Slot 1 would pass its table: its rows of out and lse keep what they held, the others
+    are those of a call that makes its own."""
+    g = torch.Generator().manual_seed(9)
+    q, k, v = (torch.randn((12, h, d), generator=g).to(torch.bfloat16).cuda() for h, d in ((8, 192), (2, 192), (2, 128)))
+    cache = PagedCache(1, 16, 16, 3, 2, 2, window=window)
+    cache.extend(ints([5, 40, 4]).cuda())
+    cu = ints([0, 5, 8, 12]).cuda()
+    want, want_lse = cache.attend(0, q, k, v, cu, 5, None, out_dtype=torch.float32)
+    out, lse = torch.full((12, 8, 128), 7.0, device="cuda"), torch.full((8, 12), 7.0, device="cuda")
+    got = cache.attend(0, q, k, v, cu, 5, None, out=out, lse=lse)
+    assert got[0] is out or got[0].data_ptr() == out.data_ptr()
+    with pytest.raises(mimo.MimoAttnError) as e:
+        mimo.mimo_attn_device_status()
+    assert e.value.status == mimo.MIMO_ERR_INVALID_ARG
+    assert torch.all(out[5:8] == 7) and torch.all(lse[:, 5:8] == 7)
+    for rows in (slice(0, 5), slice(8, 12)):
+        assert torch.isfinite(out[rows]).all() and torch.equal(out[rows], want[rows])
+        assert torch.equal(lse[:, rows], want_lse[:, rows])

@@ -21,6 +21,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import functools
+import importlib.machinery
 import math
 import os
 
@@ -443,11 +444,12 @@ def mimo_attn_prefill_backward(q, k, v, out, lse, dout, sinks, window, cu_seqlen
 
 def _load_fast():
     """The native part of the binding (csrc/fast_call.cpp) on the loaded library, or None
-    where it was not built: the calls then go through the marshalling below."""
-    try:
-        from . import _fast_call
-    except ImportError:
+    where it was not built: the calls then go through the marshalling below.  One that is
+    there and does not load (built against another torch) is an error."""
+    if not any(os.path.exists(os.path.join(_PKG, "_fast_call" + s)) for s in importlib.machinery.EXTENSION_SUFFIXES):
         return None
+    from . import _fast_call
+
     _fast_call.bind(*(ctypes.cast(getattr(lib, f"mimo_attn_{name}"), ctypes.c_void_p).value for name in (
         "paged_attention", "paged_attention_workspace_size", "paged_append", "page_hold",
         "page_hold_workspace_size", "page_fork", "page_compact", "page_compact_workspace_size", "page_copy")))

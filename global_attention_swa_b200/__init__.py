@@ -503,9 +503,23 @@ def _int(x, name):
     return x
 
 
+def _new(like, shape, stream, dtype=None):
+    """An uninitialised tensor beside ``like`` for a call on ``stream`` (None: the current
+    one).  Its memory comes from that stream's, so no work still pending elsewhere writes
+    it; and it is not given out again before the current stream, where the caller reads
+    the result, has come past its end."""
+    if stream is None or not like.is_cuda:
+        return like.new_empty(shape, dtype=dtype)
+    current = torch.cuda.current_stream(like.device)
+    with torch.cuda.stream(stream):
+        t = like.new_empty(shape, dtype=dtype)
+    t.record_stream(current)
+    return t
+
+
 def _other_stream(stream, *tensors):
-    """Tensors allocated here on the current stream and used on ``stream``: their memory is
-    not given out again before ``stream`` is past the call."""
+    """Tensors that are used on ``stream``, wherever they were made: their memory is not
+    given out again before ``stream`` is past the call."""
     if stream is not None:
         for t in tensors:
             if t is not None:
@@ -554,9 +568,9 @@ def mimo_attn_paged_attention(q, k_pages, v_pages, block_table, cu_seqlens_q, se
              _addr(cu_seqlens_q, "cu_seqlens_q", _I32, (B + 1,), dev), _addr(seqlens, "seqlens", _I32, (B,), dev))
     sink = _addr(sinks, "sinks", _F32, (hq,), dev)
     if out is None:
-        out = q.new_empty((nt, hq, dv), dtype=out_dtype)
+        out = _new(q, (nt, hq, dv), stream, out_dtype)
     if lse is None and return_lse:
-        lse = q.new_empty((hq, nt), dtype=_F32)
+        lse = _new(q, (hq, nt), stream, _F32)
     max_seqlen_q, window = _int(max_seqlen_q, "max_seqlen_q"), _int(window, "window")
     dims = _dims_ref(hq, hkv, dqk, dv, None if softmax_scale is None else float(softmax_scale), float(v_scale),
                      out.dtype)
@@ -566,7 +580,7 @@ def mimo_attn_paged_attention(q, k_pages, v_pages, block_table, cu_seqlens_q, se
         ws = _addr(workspace, "workspace", workspace.dtype, workspace.shape, dev)
         wbytes = workspace.numel() * workspace.element_size()
     elif need:
-        workspace, wbytes = block_table.new_empty(need + 3 >> 2), need
+        workspace, wbytes = _new(block_table, need + 3 >> 2, stream), need
         ws = workspace.data_ptr()
     _call(lib.mimo_attn_paged_attention, dev, dims, *addrs, B, nt, max_seqlen_q, P, ps, M, window, sink,
           _addr(out, "out", out.dtype if out.dtype in _OUT else _OUT, (nt, hq, dv), dev),
@@ -588,7 +602,7 @@ def mimo_attn_paged_append(q, k_new, v_new, k_pages, v_pages, block_table, cu_se
     P, ps, hkv, _, dv, B, M = _paged_pools(k_pages, v_pages, block_table)
     dev = q.device
     if q_out is None:
-        q_out = q.new_empty((nt, hq, dqk))
+        q_out = _new(q, (nt, hq, dqk), stream)
     _call(lib.mimo_attn_paged_append, dev, _dims_ref(hq, hkv, dqk, dv),
           _addr(q, "q", _BF16, (nt, hq, dqk), dev), _addr(q_out, "q_out", _BF16, (nt, hq, dqk), dev),
           _addr(k_new, "k_new", _BF16, (nt, hkv, dqk), dev), _addr(v_new, "v_new", _BF16, (nt, hkv, dv), dev),
@@ -607,10 +621,10 @@ def _page_table(page_refs, block_table):
     return (page_refs.shape[0], *block_table.shape)
 
 
-def _page_workspace(workspace, need, like):
+def _page_workspace(workspace, need, like, stream):
     """(tensor, address, bytes) of the caller's workspace, or of a new one beside ``like``."""
     if workspace is None:
-        workspace = like.new_empty(need + 3 >> 2)
+        workspace = _new(like, need + 3 >> 2, stream)
         return workspace, workspace.data_ptr(), need
     return (workspace, _addr(workspace, "workspace", workspace.dtype, workspace.shape, like.device),
             workspace.numel() * workspace.element_size())
@@ -633,11 +647,11 @@ def mimo_attn_page_hold(page_refs, block_table, seqlens, page_size, first=None, 
             return _taken(r)
     P, B, M = _page_table(page_refs, block_table)
     dev = page_refs.device
-    refs_out = page_refs.new_empty((P,)) if refs_out is None else refs_out
-    table_out = page_refs.new_empty((B, M)) if table_out is None else table_out
-    moves = page_refs.new_empty((B, 2)) if moves is None else moves
-    info = page_refs.new_empty((2,)) if info is None else info
-    ws, ws_addr, ws_bytes = _page_workspace(workspace, lib.mimo_attn_page_hold_workspace_size(P), page_refs)
+    refs_out = _new(page_refs, (P,), stream) if refs_out is None else refs_out
+    table_out = _new(page_refs, (B, M), stream) if table_out is None else table_out
+    moves = _new(page_refs, (B, 2), stream) if moves is None else moves
+    info = _new(page_refs, (2,), stream) if info is None else info
+    ws, ws_addr, ws_bytes = _page_workspace(workspace, lib.mimo_attn_page_hold_workspace_size(P), page_refs, stream)
     _call(lib.mimo_attn_page_hold, dev, _addr(page_refs, "page_refs", _I32, (P,), dev), P,
           _addr(block_table, "block_table", _I32, (B, M), dev), B, M, _int(page_size, "page_size"),
           _addr(seqlens, "seqlens", _I32, (B,), dev), _addr(first, "first", _I32, (B,), dev),
@@ -661,8 +675,8 @@ def mimo_attn_page_fork(page_refs, block_table, parent, refs_out=None, table_out
     P, B, M = _page_table(page_refs, block_table)
     n = parent.shape[0]
     dev = page_refs.device
-    refs_out = page_refs.new_empty((P,)) if refs_out is None else refs_out
-    table_out = page_refs.new_empty((n, M)) if table_out is None else table_out
+    refs_out = _new(page_refs, (P,), stream) if refs_out is None else refs_out
+    table_out = _new(page_refs, (n, M), stream) if table_out is None else table_out
     _call(lib.mimo_attn_page_fork, dev, _addr(page_refs, "page_refs", _I32, (P,), dev), P,
           _addr(block_table, "block_table", _I32, (B, M), dev), B, M, _addr(parent, "parent", _I32, (n,), dev), n,
           _addr(refs_out, "refs_out", _I32, (P,), dev), _addr(table_out, "table_out", _I32, (n, M), dev), stream)
@@ -685,11 +699,11 @@ def mimo_attn_page_compact(page_refs, block_table, max_moves, refs_out=None, tab
     P, B, M = _page_table(page_refs, block_table)
     max_moves = _int(max_moves, "max_moves")
     dev = page_refs.device
-    refs_out = page_refs.new_empty((P,)) if refs_out is None else refs_out
-    table_out = page_refs.new_empty((B, M)) if table_out is None else table_out
-    moves = page_refs.new_empty((max_moves, 2)) if moves is None else moves
-    info = page_refs.new_empty((2,)) if info is None else info
-    ws, ws_addr, ws_bytes = _page_workspace(workspace, lib.mimo_attn_page_compact_workspace_size(P), page_refs)
+    refs_out = _new(page_refs, (P,), stream) if refs_out is None else refs_out
+    table_out = _new(page_refs, (B, M), stream) if table_out is None else table_out
+    moves = _new(page_refs, (max_moves, 2), stream) if moves is None else moves
+    info = _new(page_refs, (2,), stream) if info is None else info
+    ws, ws_addr, ws_bytes = _page_workspace(workspace, lib.mimo_attn_page_compact_workspace_size(P), page_refs, stream)
     _call(lib.mimo_attn_page_compact, dev, _addr(page_refs, "page_refs", _I32, (P,), dev), P,
           _addr(block_table, "block_table", _I32, (B, M), dev), B, M, max_moves,
           _addr(refs_out, "refs_out", _I32, (P,), dev), _addr(table_out, "table_out", _I32, (B, M), dev),

@@ -173,3 +173,51 @@ def test_rows_of_skipped_sequences_stay_as_the_caller_had_them(window):
     for rows in (slice(0, 5), slice(8, 12)):
         assert torch.isfinite(out[rows]).all() and torch.equal(out[rows], want[rows])
         assert torch.equal(lse[:, rows], want_lse[:, rows])
+
+
+def test_tensors_made_for_another_stream_are_not_memory_still_in_use():
+    """A call on a stream of the caller's beside pending work on the current one: what it
+    makes does not lie over a tensor that the pending work writes, though that was freed."""
+    x = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in build([900, 60], [6, 6], 0, 16, 16, 1, 3).items()}
+    x["kp"], x["vp"] = x["kp"].nan_to_num(0.0), x["vp"].nan_to_num(0.0)
+    args = [x[k] for k in ("q", "kp", "vp", "table", "cu", "lens", "most", "window", "sinks")]
+    g = torch.Generator().manual_seed(1)
+    kv = [torch.randn((12, 1, d), generator=g).bfloat16().cuda() for d in (192, 128)]
+    kp, vp = x["kp"].clone(), x["vp"].clone()
+    refs, table, lens, parent = (ints(v).cuda() for v in ([1, 0, 1, 0, 0], [[2, 0, -1]], [48], [0, 0]))
+    need = mimo.mimo_attn_paged_attention_workspace_size(16, 1, 2, 12, 6)
+    side = torch.cuda.Stream()
+
+    def calls(stream):
+        return [*mimo.mimo_attn_paged_attention(*args, stream=stream),
+                mimo.mimo_attn_paged_append(x["q"], *kv, kp, vp, *args[3:6], 1e4, stream=stream),
+                *mimo.mimo_attn_page_hold(refs, table, lens, 16, stream=stream),
+                *mimo.mimo_attn_page_fork(refs, table, parent, stream=stream),
+                *mimo.mimo_attn_page_compact(refs, table, 2, stream=stream)]
+
+    want = calls(None)
+    torch.cuda.synchronize()
+    for make in (lambda: mimo.mimo_attn_paged_attention(*args, stream=side),
+                 lambda: [mimo.mimo_attn_paged_append(x["q"], *kv, kp, vp, *args[3:6], 1e4, stream=side)],
+                 lambda: mimo.mimo_attn_page_hold(refs, table, lens, 16, stream=side),
+                 lambda: mimo.mimo_attn_page_fork(refs, table, parent, stream=side),
+                 lambda: mimo.mimo_attn_page_compact(refs, table, 2, stream=side)):
+        first = make()
+        torch.cuda.synchronize()
+        first = [t.clone() for t in first]
+        torch.cuda.synchronize()
+        gone = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in (need, *[t.nbytes for t in first], *[512] * 8)]
+        torch.cuda._sleep(200_000_000)
+        for t in gone:
+            t.fill_(7)
+        del t, gone
+        got = make()
+        side.synchronize()
+        torch.cuda.synchronize()
+        for a, b in zip(got, first):
+            assert torch.equal(a, b)
+    got = calls(side)
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    mimo.mimo_attn_device_status()

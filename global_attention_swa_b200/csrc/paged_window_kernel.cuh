@@ -71,48 +71,108 @@ __device__ __forceinline__ PgTile pw_keys(const PgItem& it) { return pg_keys(it,
 // against 72.5 us).
 __device__ __forceinline__ bool pw_open(const PgItem& it) { return it.outer; }
 
+// The row of the pool's keys and values (of the item's head) at position j; -1 without a page.
+__device__ __forceinline__ long long pw_pool_row(const PagedAttnParams& p, const PgItem& it, int j) {
+  const int e = p.pb.table[(size_t)it.b * p.pb.max_pages + j / p.pb.page_size];
+  return e >= 0 && e < p.pb.num_pages ? ((long long)e * p.pb.page_size + j % p.pb.page_size) * p.Hkv + it.g : -1;
+}
+
+// Of the 32 keys from k on, those that enter the item's product with a value that is
+// not finite (bit i: key k + i).  By a whole warp.
+__device__ __forceinline__ uint32_t pw_not_finite(const PagedAttnParams& p, const PgItem& it, const PgTile& keys, int k) {
+  const int lane = threadIdx.x & 31, j = k + lane;
+  const bool in = pw_open(it) ? j >= it.lo && j <= it.hi : j < keys.k0 + keys.n;
+  const long long row = in ? pw_pool_row(p, it, j) : -1;
+  uint32_t found = 0;
+#pragma unroll 8
+  for (int i = 0; i < 32; ++i) {
+    const long long r = __shfl_sync(0xffffffffu, row, i);
+    const uint2 v = r >= 0 ? reinterpret_cast<const uint2*>(p.v + r * 128)[lane] : make_uint2(0u, 0u);
+    if (__any_sync(0xffffffffu, bf16x2_not_finite(v.x) || bf16x2_not_finite(v.y))) found |= 1u << i;
+  }
+  return found;
+}
+
 // One row (packed row tok, head h, position pos) from the definition, its output
-// only: keys that it does not see take no part at all.  For rows whose product
-// over the item's keys is not finite.  (Looking the values over as they come
-// instead, one warp ahead of the products, cost 23 us of a 69 us call; a test of
-// the products, 2 at most.)
-__device__ __noinline__ void pw_row_again(const PagedAttnParams& p, const PgItem& it, int tok, int h, int pos) {
+// only: keys that it does not see take no part at all.  For rows whose product over
+// the item's keys is not finite, where that of a key they do not see is to blame.  By
+// a whole warp: 32 keys at a time, a lane to each for its score, then four value
+// columns to a lane.  (Looking the values over as they come instead, one warp ahead of
+// the products, cost 23 us of a 69 us call; a test of the products, 2 at most.)
+__device__ __forceinline__ void pw_row_again(const PagedAttnParams& p, const PgItem& it, int tok, int h, int pos) {
   if (!MIMO_ROW_OK((long long)tok * p.Hq + h, (long long)p.pb.total_q * p.Hq)) return;
-  const uint32_t* q = reinterpret_cast<const uint32_t*>(p.q + ((size_t)tok * p.Hq + h) * 192);
+  const int lane = threadIdx.x & 31;
+  const uint4* q = reinterpret_cast<const uint4*>(p.q + ((size_t)tok * p.Hq + h) * 192);
   float m = p.sinks ? p.sinks[h] * 1.4426950408889634f : -INFINITY;
   float l = p.sinks ? 1.f : 0.f;
-  float o[128];
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-  for (int d = 0; d < 128; ++d) o[d] = 0.f;
-#pragma unroll 1
-  for (int j = max(0, pos - p.window + 1); j <= pos; ++j) {
-    const int e = p.pb.table[(size_t)it.b * p.pb.max_pages + j / p.pb.page_size];
-    const bool page = e >= 0 && e < p.pb.num_pages;  // without one: zero key and value
-    const size_t row = page ? ((size_t)e * p.pb.page_size + j % p.pb.page_size) * p.Hkv + it.g : 0;
-    const uint32_t* k = reinterpret_cast<const uint32_t*>(p.k + row * 192);
-    const uint32_t* v = reinterpret_cast<const uint32_t*>(p.v + row * 128);
+  for (int j0 = max(0, pos - p.window + 1); j0 <= pos; j0 += 32) {
+    const int j = j0 + lane;
+    const long long row = j <= pos ? pw_pool_row(p, it, j) : -1;  // without a page: zero key and value
     float s = 0.f;
-#pragma unroll 1
-    for (int i = 0; page && i < 96; ++i) s += bf16_lo(q[i]) * bf16_lo(k[i]) + bf16_hi(q[i]) * bf16_hi(k[i]);
-    s *= p.scale_log2;
-    const float up = fmaxf(m, s), neg = up == -INFINITY ? 0.f : -up;
+    if (row >= 0) {
+      const uint4* k = reinterpret_cast<const uint4*>(p.k + row * 192);
+#pragma unroll 8
+      for (int i = 0; i < 24; ++i) {
+        const uint4 a = q[i], b = k[i];
+        s += bf16_lo(a.x) * bf16_lo(b.x) + bf16_hi(a.x) * bf16_hi(b.x);
+        s += bf16_lo(a.y) * bf16_lo(b.y) + bf16_hi(a.y) * bf16_hi(b.y);
+        s += bf16_lo(a.z) * bf16_lo(b.z) + bf16_hi(a.z) * bf16_hi(b.z);
+        s += bf16_lo(a.w) * bf16_lo(b.w) + bf16_hi(a.w) * bf16_hi(b.w);
+      }
+    }
+    s = j <= pos ? s * p.scale_log2 : -INFINITY;
+    float up = fmaxf(m, s);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, d));
+    const float neg = up == -INFINITY ? 0.f : -up;
     const float f = ex2(m + neg), pe = ex2(s + neg);
+    float sum = pe;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
     m = up;
-    l = l * f + pe;
-#pragma unroll 1
-    for (int i = 0; i < 64; ++i) {
-      o[2 * i] = o[2 * i] * f + (page ? pe * bf16_lo(v[i]) : 0.f);
-      o[2 * i + 1] = o[2 * i + 1] * f + (page ? pe * bf16_hi(v[i]) : 0.f);
+    l = l * f + sum;
+    o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+#pragma unroll 16
+    for (int i = 0; i < 32; ++i) {  // past the last key: weight 0, no row
+      const float w = __shfl_sync(0xffffffffu, pe, i);
+      const long long r = __shfl_sync(0xffffffffu, row, i);
+      const uint2 v = r >= 0 ? reinterpret_cast<const uint2*>(p.v + r * 128)[lane] : make_uint2(0u, 0u);
+      o.x += w * bf16_lo(v.x);
+      o.y += w * bf16_hi(v.x);
+      o.z += w * bf16_lo(v.y);
+      o.w += w * bf16_hi(v.y);
     }
   }
   const float f = l != 0.f ? p.v_scale / l : 0.f;
-  const size_t ob = ((size_t)tok * p.Hq + h) * 128;
+  const size_t ob = ((size_t)tok * p.Hq + h) * 32 + lane;
+  if (p.out_f32)
+    reinterpret_cast<float4*>(p.out)[ob] = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+  else
+    reinterpret_cast<uint2*>(p.out)[ob] = make_uint2(pack_bf16(o.x * f, o.y * f), pack_bf16(o.z * f, o.w * f));
+}
+
+// The rows of a warp (token a of block blk, head hh of the item's) whose product is not
+// finite: done again where a key that the row does not see is to blame.
+__device__ __noinline__ void pw_rows_again(const PagedAttnParams& p, const PgItem& it, int blk, int a, int hh, bool odd) {
+  const PgTile keys = pw_keys(it);
+  const int pos0 = it.p0 + blk * p.TQ, pos = pos0 + a;
+  const int c_lo = max(pos - p.window + 1, 0) - keys.k0, c_hi = pos - keys.k0;  // what the row sees
+  bool hidden = false;
 #pragma unroll 1
-  for (int d = 0; d < 128; ++d) {
-    if (p.out_f32)
-      reinterpret_cast<float*>(p.out)[ob + d] = o[d] * f;
-    else
-      reinterpret_cast<__nv_bfloat16*>(p.out)[ob + d] = __float2bfloat16_rn(o[d] * f);
+  for (int c = 0; c < keys.n; c += 32) {
+#pragma unroll 1
+    for (uint32_t left = pw_not_finite(p, it, keys, keys.k0 + c); left; left &= left - 1) {
+      const int k = c + __ffs(left) - 1;
+      hidden |= k < c_lo || k > c_hi;
+    }
+  }
+#pragma unroll 1
+  for (uint32_t again = __ballot_sync(0xffffffffu, hidden && odd); again; again &= again - 1) {
+    const int src = __ffs(again) - 1;
+    const int a_ = __shfl_sync(0xffffffffu, a, src), h = it.g * p.G + __shfl_sync(0xffffffffu, hh, src);
+    pw_row_again(p, it, it.tok0 + blk * p.TQ + a_, h, pos0 + a_);
   }
 }
 
@@ -534,11 +594,11 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         }
         // 0 * v is NaN where v is not finite, so such a value of a key that the row
         // does not see, and another row of the item does, is in its sum
-        if (odd != 0.f) pw_row_again(p, it, tok, hg, it.p0 + blk * p.TQ + a);
+        if (__any_sync(0xffffffffu, odd != 0.f)) pw_rows_again(p, it, blk, a, hh, odd != 0.f);
         if (live && p.lse)
           p.lse[(size_t)hg * p.pb.total_q + tok] =
               (mlv.y != 0.f) ? (mlv.x * 0.6931471805599453f + logf(mlv.y)) : -INFINITY;
-        __syncwarp();  // the rows done again take their own time
+        __syncwarp();
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&i_empty[item % kPgItems]);

@@ -932,7 +932,7 @@ mimo::PagedBatch paged_batch(const int32_t* block_table, const int32_t* cu_seqle
 //   decode  one token, G <= 16: warp-level MMAs, two CTAs to an SM (64 sequences
 //           of 1024 to 32768 keys 527 us, by tiles 536; window 129 12 and 21)
 //   window  all keys of one or two blocks of 128 / G tokens fit a score tile
-//           (window 129, 5600 tokens: 72 us, by tiles 159; one block 79)
+//           (window 129, 5197 tokens: 70 us, by tiles 159; one block 79)
 //   tile    one tile of 128 / G tokens, or two that share their key tiles (1 to 6
 //           tokens at up to 16384 keys: 133 and 171 us; 2048 at 32768: 2.43 and
 //           2.28 ms)
@@ -947,7 +947,7 @@ struct PagedVariant {
 // Under a short window an item has at most four key tiles (boxes of 16 keys:
 // the window, the item's other tokens and at most 15 keys before them), and
 // only whole items are dealt out: joining parts would cost more than the
-// shares' imbalance (window 300: 5600 tokens 186 us, cut 220; 20 tokens of 4
+// shares' imbalance (window 300: 5197 tokens 186 us, cut 220; 20 tokens of 4
 // sequences 14.9 and 21.5; window 129, one token of 64 sequences: 12.3 and 14.3).
 constexpr int kPagedShortWindow = 512;
 PagedVariant paged_variant(const mimo_attn_dims_t* dims, int max_seqlen_q, int window) {

@@ -42,11 +42,18 @@
 //              tokens, 697 MB in 133 us, 5.2 TB/s (80 % of a plain copy's rate).
 //              CTAs of equal shares end between 109 and 127 us.
 //   two tiles  the products and, beside them, the exponentials: 2048 tokens at
-//              length 32768, 2.66 TFLOP in 2.28 ms, 1170 TFLOP/s (70 % of a large
-//              bf16 GEMM's burst rate; 2.5 ms, 75 % of its sustained rate, where
-//              power holds the clocks down).  Tensor pipe 55 %, XU pipe 44 %
+//              length 32768, 2.66 TFLOP in 2.28 to 2.33 ms, 1140 to 1170 TFLOP/s (70 %
+//              of a large bf16 GEMM's burst rate; 2.5 ms, 75 % of its sustained rate,
+//              where power holds the clocks down).  Tensor pipe 55 %, XU pipe 44 %
 //              active: per pair of 128 x 128 score tiles the exponentials take
 //              about as long as the products, and each softmax waits for its scores.
+//              A second chain runs beside that: V has one stage, so the next tile's
+//              values are asked for when both products of this one are done.
+//   short      (a window past what paged_window_kernel takes) 5197 new tokens under a
+//              window of 300: 186 us against 36 for the bytes.  Two of an item's three
+//              tiles are looked over between V's load and its product (pg_look), with
+//              one stage of V, and with one Q and one O an item's steps run mostly one
+//              after the other.
 #pragma once
 
 #include "paged_common.cuh"

@@ -51,7 +51,9 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volati
 // wait_bounded for a whole warp, polled by every lane, with one answer for all of
 // them.  Lanes leave the poll one by one, and where time runs out some may have seen
 // the phase and others not; what follows such a wait is done by the whole warp at
-// once (TMEM accesses, ldmatrix, votes), and needs every lane there.
+// once (TMEM accesses, ldmatrix, votes), and needs every lane there.  (A long chunk
+// takes 0.4 % more with the vote, and nothing shows elsewhere; polled by one lane and
+// passed on, a step under a short window takes 93 us for 83.)
 __device__ __forceinline__ bool wait_lanes(uint64_t* bar, uint32_t parity, volatile int* abort) {
   return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort));
 }

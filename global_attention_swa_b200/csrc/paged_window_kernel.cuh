@@ -12,12 +12,14 @@
 // so the roles run as a pipeline over blocks: while one block's softmax runs, the
 // next one's scores are computed and the queries of the one after are on their way.
 //
-// Measured on one B200 (64 query heads, 4 key/value heads, window 129, 5600 new
-// tokens of 9 sequences, 229 MB): 69.5 us, 3.3 TB/s, 50 % of a plain copy's rate
-// (the general kernel: 159 us; one block to an item, at 72 for two: 79 us).  Bound
-// by the chain of one block, scores (0.8 us), softmax (2.2), P V (0.6), of which
-// two are under way at once: P lies over its scores, and TMEM holds two score tiles
-// of 160 columns beside O.
+// Measured on one B200 (64 query heads, 4 key/value heads, window 129, 5197 new
+// tokens of 9 sequences, 229 MB): 69.5 us, 3.3 TB/s, 50 % of a plain copy's rate, and
+// up to 84 us from box to box (the general kernel: 159 us; one block to an item, at 72
+// for two: 79 us).  A CTA passes 17.6 blocks, about 4 us each.  Two chains bind: of one
+// block, scores (0.8 us), softmax (2.2), P V (0.6), with two blocks under way, since P
+// lies over its scores; and of the one O, whose next P V waits until the epilogue has
+// read both halves, the first of them stored before the second is read.  TMEM holds
+// two score tiles of 160 columns beside one O.
 //
 //   warp 12     loads Q (two buffers, a block ahead) and K (once per item, a
 //               lane per box of 16 keys; the page table is looked up here)
@@ -98,7 +100,9 @@ __device__ __forceinline__ uint32_t pw_not_finite(const PagedAttnParams& p, cons
 // the item's keys is not finite, where that of a key they do not see is to blame.  By
 // a whole warp: 32 keys at a time, a lane to each for its score, then four value
 // columns to a lane.  (Looking the values over as they come instead, one warp ahead of
-// the products, cost 23 us of a 69 us call; a test of the products, 2 at most.)
+// the products, cost 23 us of a 69 us call; a test of the products, 2 at most.)  One
+// NaN in a chunk of 165 tokens takes a 77 us call to 2.4 ms: 128 rows to a block, 20 us
+// each, 32 one after the other; by one thread a row, and for seen values too, 26 ms.
 __device__ __forceinline__ void pw_row_again(const PagedAttnParams& p, const PgItem& it, int tok, int h, int pos) {
   if (!MIMO_ROW_OK((long long)tok * p.Hq + h, (long long)p.pb.total_q * p.Hq)) return;
   const int lane = threadIdx.x & 31;

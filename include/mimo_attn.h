@@ -362,7 +362,12 @@ size_t mimo_attn_paged_attention_workspace_size(const mimo_attn_dims_t* dims, in
  * window > 0.
  *
  *   q            [total_q, Hq, Dqk] bf16, post-RoPE
- *   max_seqlen_q >= every n_b (not read back from the device), <= total_q
+ *   max_seqlen_q >= every n_b (not read back from the device), <= total_q.  One
+ *                kernel and tile size serve the whole call and are chosen by it, so
+ *                a bound above what the sequences bring costs time: 64 single
+ *                tokens over 1024 to 32768 keys take 526 us with a bound of 1, 533
+ *                with 2, 552 with 8 and 920 with 9 (64 query heads, 4 key/value
+ *                heads), and a long chunk puts single tokens beside it in its tiles
  *   window       0 = global; >= 1 = the query plus window-1 earlier keys
  *   sinks        [Hq] fp32 or NULL
  *   out          [total_q, Hq, Dv] in dims->out_dtype
@@ -412,7 +417,9 @@ mimo_status_t mimo_attn_paged_append(const mimo_attn_dims_t* dims, const void* q
  * block_table_out may be block_table (in place); otherwise the outputs must
  * not overlap the inputs.  Results are deterministic.  block_table entries at
  * or above num_pages are recorded as MIMO_ERR_INVALID_ARG and count as no page
- * (fork and compact pass them on), as is a held page whose count is not positive.
+ * (fork and compact pass them on).  page_refs has to agree with the table: a page
+ * that hold or fork takes from a row although its count is not positive is recorded
+ * too, but such a count is not looked for in pages that stay where they are.
  *
  * mimo_attn_page_hold: afterwards sequence b holds the pages of entries
  * first[b] / page_size .. ceil(seqlens[b] / page_size) - 1 and no others.
@@ -428,8 +435,8 @@ mimo_status_t mimo_attn_paged_append(const mimo_attn_dims_t* dims, const void* q
  *   info       [2] int32: pages that were missing, pages free afterwards
  * Releases come first; then the entries that need a page get the free pages,
  * lowest index first, in order of (sequence, entry).  If they do not suffice,
- * info[0] > 0 says by how many and nothing else changes (counts and table are
- * as before, no moves).  A sequence with a negative seqlens, first or write_from,
+ * info[0] > 0 says by how many and nothing else changes (counts and the pages in the
+ * table are as before, no moves; an entry that names no page may be -1 then).  A sequence with a negative seqlens, first or write_from,
  * or seqlens > max_pages * page_size, keeps its pages as they are and is recorded
  * as MIMO_ERR_INVALID_ARG.
  *

@@ -31,7 +31,9 @@ class PagedCache:
 
     ``window`` > 0 (the layers' sliding window) lets ``extend`` release the pages that no
     later query sees.  ``truncate`` can then take back the tokens of the last
-    ``extend``, and ``rollback`` more: the pages that the windows of those would see are kept."""
+    ``extend``, and ``rollback`` more: the pages that the windows of those would see are
+    kept.  What an earlier ``extend`` released does not come back: going back in several
+    steps, extending between, reaches no further."""
 
     def __init__(self, num_layers, num_pages, page_size, num_seqs, max_pages, num_heads_kv=4, head_dim_qk=192,
                  head_dim_v=128, window=0, rollback=0, device="cuda"):
@@ -107,8 +109,9 @@ class PagedCache:
 
     def truncate(self, lens):
         """Take the sequences back to lens [num_seqs] int32 (at most their present length):
-        pages behind that are released.  With a window: not below the length before the
-        last ``extend`` less ``rollback``, or to 0."""
+        pages behind that are released.  With a window: not below the greatest length
+        that the sequence had before an ``extend`` (since it was empty) less ``rollback``,
+        or to 0."""
         lens = torch.minimum(lens, self.seqlens)
         # what extend kept stays, so that a later call may go back further
         self._hold(lens, self._kept if self.window else None, None)

@@ -904,7 +904,8 @@ mimo_status_t check_paged(const int32_t* block_table, const int32_t* cu_seqlens_
     return fail(MIMO_ERR_UNSUPPORTED, "num_pages * page_size and max_pages * page_size must be at most 2^31 - 1024");
   if (max_seqlen_q > total_q)
     return fail(MIMO_ERR_INVALID_ARG, "max_seqlen_q (%d) > total_q (%d)", max_seqlen_q, total_q);
-  if (!block_table || !cu_seqlens_q || !seqlens)
+  // the tables of an empty batch have no entries, and may have no address
+  if (num_seqs > 0 && (!block_table || !cu_seqlens_q || !seqlens))
     return fail(MIMO_ERR_INVALID_ARG, "block_table, cu_seqlens_q and seqlens must be non-NULL");
   if (!aligned4(block_table) || !aligned4(cu_seqlens_q) || !aligned4(seqlens))
     return fail(MIMO_ERR_INVALID_ARG, "block_table, cu_seqlens_q and seqlens must be 4-byte aligned");

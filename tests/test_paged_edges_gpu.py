@@ -1,11 +1,13 @@
 """Edges of the paged cache on the GPU: rows of one warp that part ways, slots that
-nothing sees, sinks far below the scores, windows longer than a sequence, and turns in
-the life of a PagedCache.  Inputs and tolerances as in tests/test_paged_gpu.py."""
+nothing sees, sinks far below the scores, windows longer than a sequence, empty
+batches, many heads, and turns in the life of a PagedCache.  Inputs and tolerances
+as in tests/test_paged_gpu.py."""
 
 import numpy as np
 import pytest
 import torch
 
+from oracle import paged
 from tests import parity_util as P
 from tests.test_paged_gpu import attend, build, check, ints, oracle_of
 
@@ -221,3 +223,44 @@ def test_tensors_made_for_another_stream_are_not_memory_still_in_use():
     for a, b in zip(got, want):
         assert torch.equal(a, b)
     mimo.mimo_attn_device_status()
+
+
+def test_calls_of_no_sequence():
+    """An empty batch: nothing to do, no row touched."""
+    empty = lambda *s, dt=torch.int32: torch.empty(s, dtype=dt, device="cuda")  # noqa: E731
+    kp, vp = (torch.ones((4, 16, 1, d), dtype=torch.bfloat16, device="cuda") for d in (192, 128))
+    for rows in (0, 3):
+        q = torch.ones((rows, 4, 192), dtype=torch.bfloat16, device="cuda")
+        out = torch.full((rows, 4, 128), 7.0, device="cuda")
+        args = (kp, vp, empty(0, 5), ints([0]).cuda(), empty(0))
+        got, lse = mimo.mimo_attn_paged_attention(q, *args, 0, 0, None, out=out)
+        assert got.shape == out.shape and lse.shape == (4, rows) and torch.all(out == 7)
+        qo = torch.full_like(q, 5.0)
+        mimo.mimo_attn_paged_append(q, q[:, :1].contiguous(), q[:, :1, :128].contiguous(), *args, 1e4, q_out=qo)
+        assert torch.all(qo == 5) and torch.all(kp == 1) and torch.all(vp == 1)
+    refs, table, moves, info = mimo.mimo_attn_page_hold(ints([0, 2, 0]).cuda(), empty(0, 5), empty(0), 16)
+    assert refs.tolist() == [0, 2, 0] and table.shape == (0, 5) and moves.shape == (0, 2) and info.tolist() == [0, 2]
+    refs, table = mimo.mimo_attn_page_fork(ints([0, 2]).cuda(), empty(0, 5), empty(0))
+    assert refs.tolist() == [0, 2] and table.shape == (0, 5)
+    refs, table, moves, info = mimo.mimo_attn_page_compact(ints([0, 2]).cuda(), empty(0, 5), 1)
+    assert refs.tolist() == [2, 0] and moves.tolist() == [[1, 0]] and info.tolist() == [1, 1]
+    mimo.mimo_attn_device_status()
+
+
+@pytest.mark.parametrize("hq,hkv", [(128, 1), (128, 32), (72, 24), (256, 64)])
+@pytest.mark.parametrize("rotary", [192, 128, 64, 60, 0])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_append_of_more_heads_than_a_block_holds_at_once(hq, hkv, rotary, in_place):
+    g = torch.Generator().manual_seed(hq + rotary)
+    lens, news, ps, table = [20, 3, 70], [2, 3, 1], 32, [[1, -1, -1], [0, -1, -1], [-1, -1, 2]]
+    cu = [0, 2, 5, 6]
+    q, k, v = (torch.randn((6, h, d), generator=g).to(torch.bfloat16) for h, d in ((hq, 192), (hkv, 192), (hkv, 128)))
+    kp, vp = (torch.randn((3, ps, hkv, d), generator=g).to(torch.bfloat16) for d in (192, 128))
+    rq, rk, rv = paged.paged_append(q, k, v, kp, vp, table, cu, lens, 1e4, rotary)
+    qd, kd, vd = q.cuda(), kp.cuda(), vp.cuda()
+    qo = mimo.mimo_attn_paged_append(qd, k.cuda(), v.cuda(), kd, vd, ints(table).cuda(), ints(cu).cuda(), ints(lens).cuda(),
+                                     1e4, rotary, q_out=qd if in_place else None)
+    mimo.mimo_attn_device_status()
+    for got, want in ((qo, rq), (kd, rk)):
+        assert np.all(np.abs(P.to64(got) - want) <= 2.0 ** -8 * np.abs(want) + 1e-5)
+    assert np.array_equal(P.to64(vd), rv)

@@ -1,11 +1,12 @@
-"""The largest counts of the page bookkeeping calls: refused past the documented limits
-(on the host), right up to them (on the GPU: pair arrays of 2^31 words)."""
+"""The smallest and largest counts of the calls on a paged cache: nothing at all,
+refused past the documented limits (on the host), right up to them (on the GPU: pair
+arrays of 2^31 words)."""
 
 import pytest
 import torch
 
 import global_attention_swa_b200 as mimo
-from tests.test_paged_cpu import FAKE, UNSUPPORTED, _compact, _fork, _hold, p
+from tests.test_paged_cpu import FAKE, UNSUPPORTED, _append, _attend, _compact, _fork, _hold, p
 
 I32 = torch.int32
 
@@ -74,3 +75,9 @@ def test_copy_by_the_rows_past_2_to_the_30(big):
     mimo.mimo_attn_page_copy(k, v, moves)
     mimo.mimo_attn_device_status()
     assert torch.equal(k, want[0]) and torch.equal(v, want[1])
+
+
+def test_an_empty_batch_needs_no_tables():
+    """Its tensors have no entries and no address: nothing to do, on the host."""
+    assert _attend(seqs=0, table=0, lens=0) == mimo.MIMO_OK
+    assert _append(seqs=0, lens=0) == mimo.MIMO_OK
